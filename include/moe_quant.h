@@ -344,6 +344,135 @@ mq_status moe_quant_router_logits(const uint16_t *hidden_bf16, const uint16_t *r
                                   float *logits_f32, struct ihipStream_t *stream);
 
 /*
+ * The gate of a routed layer: which experts a token takes and with which
+ * weights, from its router logits l[t, e].  In real arithmetic:
+ *   s[t, e]  = sigmoid(l), or softmax of the token's logits over all E;
+ *   c[t, e]  = s + bias[e], the selection score (without a bias the logits'
+ *              own order, which is the scores');
+ *   groups   : experts e / (E / num_groups) form a group; a group's score is the
+ *              largest c in it (group_top 1) or the sum of its two largest
+ *              (group_top 2), and the topk_groups best groups are kept, ties
+ *              to the lower group;
+ *   ids[t]   = the k largest c of the kept groups' experts, in descending
+ *              order, ties to the lower expert id;
+ *   w[t, j]  = s of the selected experts, divided by their sum if renormalize
+ *              is not 0, times scale (the bias does not enter the weights).
+ * The selection compares the scores in 64 bits, so scores that differ by less
+ * than a 32-bit rounding are still told apart.
+ * Masked experts: an expert whose logit or bias is -inf or NaN has c = -inf and
+ * weight 0.  It is selected only where fewer than k experts of the kept groups
+ * are left, lower ids first; a row without any live expert has weights 0 and k
+ * distinct valid ids.  A logit of +inf counts as the largest finite float.
+ */
+typedef enum { MQ_SCORE_SOFTMAX = 0, MQ_SCORE_SIGMOID = 1 } mq_score;
+
+typedef struct {
+  uint32_t abi_version; /* must equal MOE_QUANT_ABI_VERSION                        */
+  int32_t num_experts;  /* E, 1 to 512                                              */
+  int32_t top_k;        /* k, 1 to min(64, topk_groups * E / num_groups)            */
+  int32_t score;        /* mq_score                                                 */
+  int32_t num_groups;   /* 1 (no groups) to 64, a divisor of E                      */
+  int32_t topk_groups;  /* groups kept, 1 to num_groups                             */
+  int32_t group_top;    /* 1 or 2 (2 needs groups of two experts or more)           */
+  int32_t renormalize;
+  float scale;          /* finite                                                   */
+  const float *bias;    /* NULL, or [E] on the device, 4-byte aligned               */
+} mq_gate;
+
+/*
+ * Enqueue the gate of num_tokens tokens on `stream`.
+ *   logits   [T, E] of logits_dtype, 16-byte aligned
+ *   ids      int32 [T, k], weights float [T, k]: written, 4-byte aligned
+ * num_tokens == 0 returns MQ_OK without enqueuing anything.  No layer handle
+ * and no workspace are needed.
+ * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE (a field outside its range, scale not
+ * finite), MQ_E_DTYPE, MQ_E_ALIGN, MQ_E_HIP.
+ */
+mq_status moe_quant_gate_topk(const mq_gate *g, const void *logits, int32_t logits_dtype,
+                              int64_t num_tokens, int32_t *ids, float *weights,
+                              struct ihipStream_t *stream);
+
+/*
+ * moe_quant_forward under a gate: the experts and weights of mq_gate in the
+ * place of the softmax over the k largest logits, the rest of the path the
+ * same.  The gate's num_experts and top_k are the layer's.
+ *   router_logits  [T, E] of logits_dtype, or NULL with
+ *   router_bf16    [E, H] BF16 bits (the gate's weight): then the logits are
+ *                  computed here, as moe_quant_router_logits does
+ *   activations    mq_act: MQ_ACT_BF16 (moe_quant_forward), MQ_ACT_FP8
+ *                  (moe_quant_forward_w8a8, FP8 layers) or MQ_ACT_NVFP4
+ *                  (moe_quant_forward_w4a4, NVFP4 layers, with its act_gscales)
+ *   logits_out     NULL, or float [T, E] that receives the logits computed here
+ *   the others     as for moe_quant_forward; masked logits (-inf, NaN) are those
+ *                  of mq_gate
+ * The per-slot expert outputs are rounded to FP16 after a power of two was
+ * taken out of the token's weights, so weights of any size keep their digits.
+ * A layer of one expert with top_k 1, MQ_SCORE_SIGMOID and renormalize 0 is a
+ * shared expert with its sigmoid gate.
+ * Errors: as moe_quant_forward and moe_quant_gate_topk, MQ_E_NULL unless
+ * exactly one of router_logits and router_bf16 is given, MQ_E_SHAPE where gate
+ * and layer differ, MQ_E_FORMAT for activations that the layer's format lacks.
+ */
+typedef enum { MQ_ACT_BF16 = 0, MQ_ACT_FP8 = 1, MQ_ACT_NVFP4 = 2 } mq_act;
+
+mq_status moe_quant_forward_gated(const mq_layer *L, const mq_gate *gate, const void *router_logits,
+                                  int32_t logits_dtype, const uint16_t *router_bf16,
+                                  const uint16_t *hidden_bf16, const uint16_t *residual_bf16,
+                                  int64_t num_tokens, uint16_t *out_bf16, void *workspace,
+                                  size_t workspace_bytes, int32_t activations, float act_gscale13,
+                                  float act_gscale2, float *logits_out, const mq_probe *probe,
+                                  struct ihipStream_t *stream);
+
+/*
+ * Norms before and after a block in one pass over each row, with the block's
+ * gate, the residual scale and the residual add between them:
+ *   z  = x,  or with post_weight  x / sqrt(mean(x^2) + eps) * (offset + post_weight);
+ *   r' = round(residual + scale * gate * z)        to residual_dtype;
+ *   n  = bf16(r' / sqrt(mean(r'^2) + eps) * (offset + pre_weight)),
+ * the mean over the row's hidden values, all in FP32.  x is a block's output
+ * (the layer's, for instance), n the next block's input.  n is computed from
+ * the rounded r', so one call gives the same bits as two (x and post_weight
+ * first, then residual = r' and pre_weight).  Squares are summed in FP32:
+ * values beyond 2^55 in magnitude are outside of this entry's range.
+ */
+typedef enum {
+  MQ_GATE_NONE = 0,
+  MQ_GATE_CHANNEL = 1, /* gate [H]: one factor per channel           */
+  MQ_GATE_TOKEN = 2,   /* gate [T]: one factor per token             */
+  MQ_GATE_FULL = 3     /* gate [T, H]                                */
+} mq_gate_kind;
+
+typedef struct {
+  uint32_t abi_version;   /* must equal MOE_QUANT_ABI_VERSION              */
+  int32_t hidden;         /* H, 1 to 32768                                  */
+  int32_t residual_dtype; /* mq_dtype of residual and residual_out          */
+  int32_t weight_dtype;   /* mq_dtype of post_weight and pre_weight         */
+  float eps;              /* finite and positive                            */
+  float weight_offset;    /* finite: 0, or 1 where weights are stored as w - 1 */
+  float scale;            /* finite                                         */
+  const void *post_weight;/* NULL (no norm after the block) or [H]          */
+  const void *pre_weight; /* NULL (no norm before the next block) or [H]    */
+} mq_norm;
+
+/*
+ * Enqueue the norms of num_tokens rows on `stream`.  All arrays are 16-byte
+ * aligned, a per-token gate to its element.
+ *   x_bf16        [T, H] BF16 bits; NULL (then post_weight and gate are NULL
+ *                 and r' = residual)
+ *   residual      [T, H]; NULL counts as zero
+ *   gate          NULL for MQ_GATE_NONE, else of gate_dtype and the kind's shape
+ *   residual_out  [T, H], NULL if not wanted; may alias residual
+ *   norm_out_bf16 [T, H]: given if and only if pre_weight is; may alias x_bf16
+ * At least one of x and residual and one of the outputs is given.
+ * num_tokens == 0 returns MQ_OK without enqueuing anything.
+ * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE (a field outside its range, an unknown
+ * gate kind), MQ_E_DTYPE, MQ_E_ALIGN, MQ_E_HIP.
+ */
+mq_status moe_quant_norm(const mq_norm *n, const uint16_t *x_bf16, const void *residual,
+                         const void *gate, int32_t gate_kind, int32_t gate_dtype, int64_t num_tokens,
+                         void *residual_out, uint16_t *norm_out_bf16, struct ihipStream_t *stream);
+
+/*
  * Allocation-free variant of moe_quant_forward, for callers that cannot
  * allocate device memory: code under HIP graph capture, tight serving loops,
  * harnesses that forbid allocation.  It runs the same kernels; their scratch

@@ -13,7 +13,9 @@ of what the GPU path computes:
 * ``formats`` - the three packed weight formats (INT4 g128, FP8 128x128 block,
   NVFP4 per-16) with their quantizers, packers and dequantizers;
 * ``moe``     - router top-k + softmax, stable permutation, the per-expert
-  SwiGLU loop and the slot-ordered combine.
+  SwiGLU loop and the slot-ordered combine;
+* ``gate``    - gated routing (scores, balance bias, groups, top-k, weights);
+* ``norm``    - the norms before and after a block with gate and residual scale.
 
 It shares no code with the GPU path.  Parity of every function is pinned in
 ``tests/test_codecs.py`` and ``tests/test_oracle.py`` against values the model

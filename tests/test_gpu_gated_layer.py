@@ -1,0 +1,260 @@
+"""The expert layer under a gate on the GPU: routing and outputs against the
+float64 oracle, in every weight format and activation kind, and the block of
+norm, router, gate, experts, shared expert and norm as it is used."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gate as ogate
+from oracle import moe as omoe
+from oracle import norm as onorm
+from tests.gpu_helpers import ATOL_MAX, RTOL_L2, GpuLayer, dev, random_layer
+from weight_quantized_moe_amd import Gate, MoeQuantError, ResidualNorm, router_logits
+
+pytestmark = pytest.mark.gpu
+FORMATS = ["int4_g128", "fp8_b128", "nvfp4_g16"]
+BF = torch.bfloat16
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def oracle_layer(lay, ids, w, x_bits):
+    """The oracle's permute, expert loop and combine under given ids and weights."""
+    from oracle import formats
+    perm = omoe.permute(ids, lay.layer.num_experts)
+    x = omoe.bf16_bits_to_f64(x_bits)
+    out = np.empty((ids.size, lay.layer.hidden))
+    for e in range(lay.layer.num_experts):
+        lo, hi = perm.offsets[e], perm.offsets[e + 1]
+        if hi > lo:
+            out[lo:hi] = omoe.expert_mlp(x[perm.sorted_token_ids[lo:hi]], formats.dequantize_expert(lay.p13, e),
+                                         formats.dequantize_expert(lay.p2, e))
+    return omoe.combine(perm, w, out), perm
+
+
+def make(t, e, h, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rn(*s):
+        return torch.randn(*s, generator=gen, device="cuda")
+    return dict(lg=1.5 * rn(t, e) + 0.5 * rn(e), x=rn(t, h).to(BF), r=rn(t, h).to(BF), bias=0.1 * rn(e))
+
+
+def probe_for(t, lay):
+    k, e = lay.top_k, lay.layer.num_experts
+    i32 = dict(dtype=torch.int32, device="cuda")
+    return dict(topk_ids=torch.empty((t, k), **i32), topk_w=torch.empty((t, k), device="cuda"),
+                expert_offsets=torch.empty(e + 1, **i32), sorted_token_ids=torch.empty(t * k, **i32),
+                inv_pos=torch.empty(t * k, **i32))
+
+
+def check(lay, gate, kw, d, residual=True, router_w=None, **call):
+    """Ids and grouping equal the oracle's, the output to the layer's tolerance
+    (relative to the size of the weights' sum)."""
+    t = d["x"].shape[0]
+    pr, lg = probe_for(t, lay), d["lg"]
+    more = dict(logits=lg)
+    if router_w is not None:
+        lg = torch.empty((t, gate.num_experts), device="cuda")
+        more = dict(router_w=router_w, logits_out=lg)
+    out = lay.layer.forward_gated(gate, d["x"], residual=d["r"] if residual else None, probe=pr, **more, **call)
+    torch.cuda.synchronize()
+    ids, w = ogate.gate(f64(lg), lay.top_k, bias=None if gate.bias is None else f64(gate.bias), **kw)
+    assert np.array_equal(pr["topk_ids"].cpu().numpy(), ids)
+    assert np.allclose(f64(pr["topk_w"]), w, rtol=1e-5, atol=1e-30)
+    y, perm = oracle_layer(lay, ids, w, bits(d["x"]))
+    for name in ("sorted_token_ids", "inv_pos"):
+        assert np.array_equal(pr[name].cpu().numpy(), getattr(perm, name)), name
+    assert np.array_equal(pr["expert_offsets"].cpu().numpy(), perm.offsets)
+    if residual:
+        y = y + f64(d["r"])
+    got, big = f64(out), max(1.0, np.abs(w).sum(1).max())
+    rel = np.linalg.norm(got - y) / max(np.linalg.norm(y), 1e-300)
+    assert rel <= RTOL_L2 and np.abs(got - y).max() <= ATOL_MAX * big, (rel, np.abs(got - y).max())
+    return out
+
+
+GROUPED = dict(score="sigmoid", groups=4, topk_groups=2, group_top=2, scale=2.5)
+
+
+def gate_of(e, k, bias=None, **kw):
+    return Gate(e, k, bias=bias, **{("num_groups" if n == "groups" else n): v for n, v in kw.items()})
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("t", [1, 2, 3, 16, 17, 61, 300])
+@pytest.mark.parametrize("residual", [False, True])
+def test_layer(fmt, t, residual):
+    lay = GpuLayer(*random_layer(fmt, 3, 16, 256, 128), 4)
+    d = make(t, 16, 256, seed=t)
+    check(lay, gate_of(16, 4, d["bias"], **GROUPED), GROUPED, d, residual)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("t", [1, 40])
+def test_long_rows(fmt, t):
+    """Hidden rows longer than the routing stage keeps in registers."""
+    lay = GpuLayer(*random_layer(fmt, 5, 8, 2304, 128), 2)
+    kw = dict(score="softmax", renormalize=False)
+    d = make(t, 8, 2304, seed=t)
+    check(lay, gate_of(8, 2, **kw), kw, d)
+
+
+@pytest.mark.parametrize("t", [1, 5, 33, 4100])
+def test_from_the_router_weight(t):
+    """In-library logits, at every routing size; the gate is checked on the logits it
+    decided on."""
+    lay = GpuLayer(*random_layer("int4_g128", 3, 16, 256, 128), 4)
+    d = make(t, 16, 256, seed=t)
+    w = (0.1 * torch.randn(16, 256, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))).to(BF)
+    check(lay, gate_of(16, 4, d["bias"], **GROUPED), GROUPED, d, router_w=w)
+    # without logits_out the same logits are used
+    a = lay.layer.forward_gated(gate_of(16, 4, d["bias"], **GROUPED), d["x"], router_w=w)
+    b = lay.layer.forward_gated(gate_of(16, 4, d["bias"], **GROUPED), d["x"], logits=router_logits(d["x"], w))
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_more_experts_than_the_fused_router_holds():
+    lay = GpuLayer(*random_layer("fp8_b128", 3, 300, 128, 128), 3)
+    d = make(20, 300, 128)
+    w = (0.1 * torch.randn(300, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))).to(BF)
+    check(lay, gate_of(300, 3, d["bias"], score="sigmoid"), dict(score="sigmoid"), d, router_w=w)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("t", [1, 2, 16, 65, 300])
+def test_the_default_gate_is_the_layers_own_routing(fmt, t):
+    lay = GpuLayer(*random_layer(fmt, 7, 16, 256, 128), 4)
+    d = make(t, 16, 256, seed=t)
+    pr, pg = probe_for(t, lay), probe_for(t, lay)
+    a = lay.layer.forward(d["lg"], d["x"], residual=d["r"], probe=pr)
+    b = lay.layer.forward_gated(Gate(16, 4), d["x"], logits=d["lg"], residual=d["r"], probe=pg)
+    torch.cuda.synchronize()
+    for n in ("topk_ids", "expert_offsets", "sorted_token_ids", "inv_pos"):
+        assert torch.equal(pr[n], pg[n]), n
+    assert np.allclose(f64(pr["topk_w"]), f64(pg["topk_w"]), rtol=2e-6)
+    assert np.linalg.norm(f64(a) - f64(b)) <= RTOL_L2 * np.linalg.norm(f64(a))
+
+
+@pytest.mark.parametrize("t", [1, 2, 50])
+def test_weights_of_any_size_keep_their_digits(t):
+    """Weights far below what FP16 holds: the output is the scaled output."""
+    lay = GpuLayer(*random_layer("int4_g128", 7, 16, 256, 128), 4)
+    d = make(t, 16, 256, seed=t)
+    kw = dict(score="sigmoid", scale=2.0 ** -40)
+    check(lay, gate_of(16, 4, **kw), kw, d, residual=False)
+    kw = dict(score="sigmoid", renormalize=False)
+    far = dict(d, lg=d["lg"] - 40.0)
+    check(lay, gate_of(16, 4, **kw), kw, far, residual=False)
+
+
+def test_masked_rows():
+    """A row without live experts gives the residual, and rows with few take
+    their live experts alone."""
+    lay = GpuLayer(*random_layer("nvfp4_g16", 7, 16, 256, 128), 4)
+    for t in (2, 12, 100):
+        d = make(t, 16, 256, seed=t)
+        d["lg"][0] = -float("inf")
+        d["lg"][1, 3:] = -float("inf")
+        for kw in (GROUPED, dict(score="softmax")):
+            out = check(lay, gate_of(16, 4, **kw), kw, d)
+            assert torch.equal(out[0], d["r"][0])
+
+
+@pytest.mark.parametrize("t", [1, 20, 300])
+def test_fp8_and_nvfp4_activations(t):
+    """The gate in front of the W8A8 and W4A4 paths: with the default gate they
+    give what forward_w8a8 and forward_w4a4 give."""
+    d = make(t, 16, 256, seed=t)
+    lay = GpuLayer(*random_layer("fp8_b128", 7, 16, 256, 128), 4)
+    a = lay.layer.forward_w8a8(d["lg"], d["x"], residual=d["r"])
+    b = lay.layer.forward_gated(Gate(16, 4), d["x"], logits=d["lg"], residual=d["r"], activations="fp8")
+    lay4 = GpuLayer(*random_layer("nvfp4_g16", 7, 16, 256, 128), 4)
+    c = lay4.layer.forward_w4a4(d["lg"], d["x"], 300.0, 900.0, residual=d["r"])
+    e = lay4.layer.forward_gated(Gate(16, 4), d["x"], logits=d["lg"], residual=d["r"], activations="nvfp4",
+                                 act_gscale13=300.0, act_gscale2=900.0)
+    torch.cuda.synchronize()
+    for p, q in ((a, b), (c, e)):
+        assert np.linalg.norm(f64(p) - f64(q)) <= RTOL_L2 * np.linalg.norm(f64(p))
+
+
+def test_refusals_and_no_tokens():
+    lay = GpuLayer(*random_layer("int4_g128", 7, 16, 256, 128), 4)
+    d = make(3, 16, 256)
+    with pytest.raises(MoeQuantError, match="picks 2 of 16"):
+        lay.layer.forward_gated(Gate(16, 2), d["x"], logits=d["lg"])
+    with pytest.raises(ValueError, match="workspace"):
+        lay.layer.forward_gated(Gate(16, 4), d["x"], logits=d["lg"], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    out = lay.layer.forward_gated(Gate(16, 4), d["x"][:0], logits=d["lg"][:0])
+    assert out.shape == (0, 256)
+
+
+@pytest.mark.parametrize("t", [1, 9, 200])
+def test_two_streams_and_graph_replays(t):
+    """Calls on two streams with workspaces of their own, and a captured call
+    replayed with other inputs between eager ones on another workspace."""
+    lay = GpuLayer(*random_layer("fp8_b128", 7, 16, 256, 128), 4)
+    d = make(t, 16, 256, seed=t)
+    gate = gate_of(16, 4, d["bias"], **GROUPED)
+    ref = lay.layer.forward_gated(gate, d["x"], logits=d["lg"])
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [lay.layer.forward_gated(gate, d["x"], logits=d["lg"], stream=s) for s in (s1, s2, s1)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref, o) for o in outs)
+    lg, out, ws = d["lg"].clone(), torch.zeros_like(d["x"]), lay.layer.workspace(t)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lay.layer.forward_gated(gate, d["x"], logits=lg, out=out, workspace=ws)
+    for r in range(3):
+        lg.copy_(make(t, 16, 256, seed=50 + r)["lg"])
+        graph.replay()
+        eager = lay.layer.forward_gated(gate, d["x"], logits=lg)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("t", [1, 7, 150])
+def test_a_block_as_it_is_used(t):
+    """norm -> router -> gated experts + shared expert -> norm after the block, gated
+    and scaled onto the residual stream -> norm before the next block."""
+    e, k, h, i = 16, 4, 256, 128
+    lay = GpuLayer(*random_layer("int4_g128", 11, e, h, i), k)
+    shared = GpuLayer(*random_layer("fp8_b128", 12, 1, h, i), 1)
+    d = make(t, e, h, seed=t)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w = lambda *s: (0.1 * torch.randn(*s, generator=gen, device="cuda")).to(BF)  # noqa: E731
+    router, shared_router = w(e, h), w(1, h)
+    norms = [1 + w(h).float() for _ in range(3)]
+    channel = 1 + w(h).float()
+    stream = d["r"].float()
+    before = ResidualNorm(h, pre_weight=norms[0], residual_dtype=torch.float32)
+    after = ResidualNorm(h, post_weight=norms[1], pre_weight=norms[2], residual_dtype=torch.float32, scale=0.5)
+    gate, sgate = gate_of(e, k, d["bias"], **GROUPED), Gate(1, 1, score="sigmoid", renormalize=False)
+    stream1, x = before.forward(d["x"], stream)
+    y_s = shared.layer.forward_gated(sgate, x, router_w=shared_router)
+    y = lay.layer.forward_gated(gate, x, router_w=router, residual=y_s)
+    stream2, nxt = after.forward(y, stream1, gate=channel)
+    torch.cuda.synchronize()
+    # each step against the oracle on the values that the step before it gave
+    assert np.allclose(f64(stream1), f64(stream) + f64(d["x"]), rtol=2.0 ** -24, atol=1e-12)
+    ref = onorm.rms_norm(f64(stream1), f64(norms[0]), 1e-6, 0.0)
+    assert np.all(np.abs(f64(x) - ref) <= (2.0 ** -8 + 1e-5) * np.abs(ref))
+    lg = f64(router_logits(x, router))
+    ids, wt = ogate.gate(lg, k, bias=f64(d["bias"]), **GROUPED)
+    ref, _ = oracle_layer(lay, ids, wt, bits(x))
+    sl = f64(router_logits(x, shared_router))
+    sref, _ = oracle_layer(shared, np.zeros((t, 1), np.int32), 1 / (1 + np.exp(-sl)), bits(x))
+    for got, want in ((y_s, sref), (y, ref + f64(y_s))):
+        assert np.linalg.norm(f64(got) - want) <= RTOL_L2 * np.linalg.norm(want)
+    r, add = onorm.residual_update(f64(y), f64(stream1), f64(channel), f64(norms[1]), scale=0.5)
+    assert np.allclose(f64(stream2), r + add, rtol=0, atol=2e-5 * np.abs(r + add).max())
+    ref = onorm.rms_norm(f64(stream2), f64(norms[2]), 1e-6, 0.0)
+    assert np.all(np.abs(f64(nxt) - ref) <= (2.0 ** -8 + 1e-5) * np.abs(ref))

@@ -1,0 +1,162 @@
+"""Norms before and after a block on the GPU against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import norm as onorm
+from weight_quantized_moe_amd import ResidualNorm
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def f64(t):
+    return None if t is None else t.float().cpu().numpy().astype(np.float64)
+
+
+def inputs(t, h, rd=BF, wd=BF, gate="none", gd=BF, seed=0, size=3.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rn(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+
+    shape = {"none": None, "channel": (h,), "token": (t, 1), "full": (t, h)}[gate]
+    return dict(x=(size * rn(t, h)).to(BF), r=(4 * rn(t, h)).to(rd),
+                g=None if shape is None else (1 + 0.5 * rn(*shape)).to(gd),
+                post=(1 + 0.1 * rn(h)).to(wd), pre=(1 + 0.1 * rn(h)).to(wd))
+
+
+def check(t, h, d, post=True, pre=True, rd=BF, eps=1e-6, offset=0.0, scale=1.0, x=True, residual=True, size=None):
+    """Elementwise bounds.  The squares' sum takes h / 64 additions in a lane and
+    about 16 across lanes and waves at most, halved by the root; a handful of
+    products follow: c = 16 + h / 64 roundings of 2^-24 of each term, and half a
+    step of the output's type.  The second norm is compared with the oracle's
+    norm of the residual that came back, which it is defined on."""
+    n = ResidualNorm(h, post_weight=d["post"] if post else None, pre_weight=d["pre"] if pre else None, eps=eps,
+                     weight_offset=offset, scale=scale, residual_dtype=rd)
+    # rows behind the last one stay as they were
+    ro = torch.full((t + 1, h), 7.0, dtype=rd, device="cuda")
+    no = torch.full((t + 1, h), 7.0, dtype=BF, device="cuda")
+    got_r, got_n = n.forward(d["x"] if x else None, d["r"] if residual else None, gate=d["g"] if x else None,
+                             residual_out=ro[:t], norm_out=no[:t] if pre else None)
+    torch.cuda.synchronize()
+    assert torch.all(ro[t:] == 7.0) and torch.all(no[t:] == 7.0) and (got_n is None) == (not pre)
+    c = (16 + h / 64) * 2.0 ** -24
+    half = torch.finfo(rd).eps / 2
+    r, add = onorm.residual_update(f64(d["x"]) if x else None, f64(d["r"]) if residual else None,
+                                   f64(d["g"]) if x else None, f64(d["post"]) if post else None, eps, offset, scale)
+    ref = r + add
+    off = np.abs(f64(got_r) - ref)
+    limit = half * np.abs(ref) * (1 + c) + c * (np.abs(r) + np.abs(add)) + 1e-38
+    assert np.all(off <= limit), (float((off / limit).max()), np.unravel_index((off / limit).argmax(), off.shape))
+    if pre:
+        ref = onorm.rms_norm(f64(got_r), f64(d["pre"]), eps, offset)
+        off, limit = np.abs(f64(got_n) - ref), (2.0 ** -8 + c) * np.abs(ref) + 1e-38
+        assert np.all(off <= limit), (float((off / limit).max()), np.unravel_index((off / limit).argmax(), off.shape))
+    return got_r, got_n
+
+
+HIDDEN = [1, 2, 7, 8, 64, 129, 256, 520, 1023, 1024, 2048, 2056, 4096, 4100, 5000, 8192, 8200, 16384, 16392, 32760, 32768]
+
+
+@pytest.mark.parametrize("h", HIDDEN)
+@pytest.mark.parametrize("rd", [BF, F32])
+def test_sizes(h, rd):
+    for t in (1, 3, 37):
+        check(t, h, inputs(t, h, rd, gate="full", seed=h), rd=rd, scale=0.5)
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("gd", [BF, F32])
+@pytest.mark.parametrize("wd", [BF, F32])
+@pytest.mark.parametrize("h", [96, 333, 2048])
+def test_gates_and_types(gate, gd, wd, h):
+    for post, pre in ((True, True), (True, False), (False, True), (False, False)):
+        for rd in (BF, F32):
+            check(5, h, inputs(5, h, rd, wd, gate, gd), post, pre, rd, offset=1.0, scale=-0.22, eps=1e-5)
+
+
+def test_without_x_or_residual():
+    for h in (64, 77, 4096):
+        d = inputs(9, h)
+        check(9, h, d, post=False, x=False)
+        check(9, h, d, residual=False)
+        check(9, h, d, pre=False, residual=False)
+        r, _ = check(9, h, d, post=False, pre=False, x=False)
+        assert torch.equal(r, d["r"])
+
+
+@pytest.mark.parametrize("h", [256, 333, 8192])
+def test_two_calls_give_the_bits_of_one(h):
+    for rd in (BF, F32):
+        d = inputs(11, h, rd, gate="channel")
+        r, n = check(11, h, d, rd=rd)
+        r1, none = ResidualNorm(h, post_weight=d["post"], residual_dtype=rd).forward(d["x"], d["r"], gate=d["g"])
+        r2, n2 = ResidualNorm(h, pre_weight=d["pre"], residual_dtype=rd).forward(None, r1)
+        assert none is None and torch.equal(r, r1) and torch.equal(r, r2) and torch.equal(n, n2)
+
+
+@pytest.mark.parametrize("h", [64, 1001, 2048, 16384])
+def test_outputs_in_the_inputs_own_buffers(h):
+    for rd in (BF, F32):
+        d = inputs(13, h, rd, gate="full")
+        r, n = check(13, h, d, rd=rd)
+        op = ResidualNorm(h, post_weight=d["post"], pre_weight=d["pre"], residual_dtype=rd)
+        x, res = d["x"].clone(), d["r"].clone()
+        op.forward(x, res, gate=d["g"], residual_out=res, norm_out=x)
+        torch.cuda.synchronize()
+        assert torch.equal(res, r) and torch.equal(x, n)
+
+
+def test_zero_rows_and_far_values():
+    h = 512
+    d = inputs(6, h)
+    d["x"][0], d["r"][0] = 0, 0
+    d["x"][1] = 2.0 ** 50
+    d["r"][2] = -(2.0 ** 50)
+    d["x"][3] = 2.0 ** -60
+    d["x"][4, 1:], d["x"][4, 0] = 0, 1e30 * 2.0 ** -60
+    r, n = check(6, h, d)
+    assert torch.all(r[0] == 0) and torch.all(n[0] == 0)
+
+
+def test_many_rows_and_none():
+    d = inputs(20000, 128, gate="token")
+    check(20000, 128, d)
+    d = inputs(1, 64)
+    op = ResidualNorm(64, post_weight=d["post"], pre_weight=d["pre"])
+    r, n = op.forward(d["x"][:0], d["r"][:0])
+    assert r.shape == (0, 64) and n.shape == (0, 64)
+
+
+def test_offsets_past_32_bits():
+    t, h = 70000, 32768                                 # 2.3e9 values
+    x = torch.zeros((t, h), dtype=BF, device="cuda")
+    d = inputs(3, h)
+    x[-3:] = d["x"]
+    op = ResidualNorm(h, post_weight=d["post"])
+    r, _ = op.forward(x)
+    small, _ = op.forward(d["x"])
+    assert torch.equal(r[-3:], small) and torch.all(r[-4] == 0)
+
+
+def test_same_bits_again_on_another_stream_and_in_a_graph():
+    h = 2048
+    d = inputs(50, h, gate="channel")
+    op = ResidualNorm(h, post_weight=d["post"], pre_weight=d["pre"])
+    r, n = op.forward(d["x"], d["r"], gate=d["g"])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    r2, n2 = op.forward(d["x"], d["r"], gate=d["g"], stream=s)
+    s.synchronize()
+    assert torch.equal(r, r2) and torch.equal(n, n2)
+    r3, n3 = torch.zeros_like(r), torch.zeros_like(n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.forward(d["x"], d["r"], gate=d["g"], residual_out=r3, norm_out=n3)
+    for seed in range(3):
+        d["x"].copy_(inputs(50, h, seed=30 + seed)["x"])
+        graph.replay()
+        r4, n4 = op.forward(d["x"], d["r"], gate=d["g"])
+        torch.cuda.synchronize()
+        assert torch.equal(r3, r4) and torch.equal(n3, n4)

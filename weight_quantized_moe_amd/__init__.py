@@ -7,13 +7,15 @@ library; constructing a :class:`Layer` does, and raises if it is missing.
 """
 from .binding import (  # noqa: F401
     FORMATS,
+    Gate,
     Layer,
     MoeQuantError,
+    ResidualNorm,
     import_expert,
     library_path,
     load_library,
     router_logits,
 )
 
-__all__ = ["FORMATS", "Layer", "MoeQuantError", "import_expert", "library_path", "load_library",
+__all__ = ["FORMATS", "Gate", "Layer", "MoeQuantError", "ResidualNorm", "import_expert", "library_path", "load_library",
            "router_logits"]

@@ -15,6 +15,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ABI_VERSION = 1
 FORMATS = {"int4_g128": 1, "fp8_b128": 2, "nvfp4_g16": 3}
 MQ_F32, MQ_BF16 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"bf16": 0, "fp8": 1, "nvfp4": 2}
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = range(4)
 STAGES = ("route", "permute", "gate_up", "down", "combine")
 
 EXPORTED = (
@@ -25,6 +28,9 @@ EXPORTED = (
     "moe_quant_forward_with_router",
     "moe_quant_forward_w8a8",
     "moe_quant_forward_w4a4",
+    "moe_quant_forward_gated",
+    "moe_quant_gate_topk",
+    "moe_quant_norm",
     "moe_quant_quantize_act",
     "moe_quant_quantize_act_nvfp4",
     "moe_quant_import_expert",
@@ -58,6 +64,35 @@ class LayerDesc(ctypes.Structure):
         ("w2", ctypes.c_void_p),
         ("w2_scale", ctypes.c_void_p),
         ("w2_gscale", ctypes.c_void_p),
+    ]
+
+
+class GateDesc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("hidden", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("post_weight", ctypes.c_void_p),
+        ("pre_weight", ctypes.c_void_p),
     ]
 
 
@@ -130,6 +165,13 @@ def load_library():
     lib.moe_quant_dequantize.restype = i32
     lib.moe_quant_router_logits.argtypes = [vp, vp, i64, i32, i32, vp, vp]
     lib.moe_quant_router_logits.restype = i32
+    lib.moe_quant_gate_topk.argtypes = [ctypes.POINTER(GateDesc), vp, i32, i64, vp, vp, vp]
+    lib.moe_quant_gate_topk.restype = i32
+    lib.moe_quant_forward_gated.argtypes = [vp, ctypes.POINTER(GateDesc), vp, i32, vp, vp, vp, i64, vp, vp, sz, i32,
+                                            f32, f32, vp, ctypes.POINTER(Probe), vp]
+    lib.moe_quant_forward_gated.restype = i32
+    lib.moe_quant_norm.argtypes = [ctypes.POINTER(NormDesc), vp, vp, vp, i32, i32, i64, vp, vp, vp]
+    lib.moe_quant_norm.restype = i32
     lib.moe_quant_destroy.argtypes = [vp]
     lib.moe_quant_destroy.restype = None
     lib.moe_quant_status_string.argtypes = [i32]
@@ -186,6 +228,23 @@ def _on_gpu(device, **tensors):
         device = device if device is not None else t.device
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _is_current(t) -> bool:
+    """Whether ``t`` is on the current GPU (a tensor elsewhere than on a GPU is
+    left to _on_gpu)."""
+    import torch
+    return not t.is_cuda or t.device.index == torch.cuda.current_device()
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on ``stream`` (None: the current one): taken from that
+    stream's memory, so no earlier tensor's work on another stream still uses it."""
+    import torch
+    if stream is None or not device.type == "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _nbytes(t) -> int:
@@ -306,6 +365,136 @@ def quantize_act_nvfp4(x, gscale: float, codes=None, scales=None, stream=None):
     return codes, scales
 
 
+def _mq_dtype(dtype) -> int:
+    import torch
+    return MQ_F32 if dtype == torch.float32 else MQ_BF16
+
+
+class Gate:
+    """The gate of a routed layer (mq_gate): softmax or sigmoid scores, a balance
+    ``bias`` (float32 [E] on the GPU) that takes part in the selection only,
+    ``topk_groups`` of ``num_groups`` groups ranked by their ``group_top`` (1 or
+    2) largest selection scores, top-k, renormalised or raw weights, times
+    ``scale``.  The bias must stay alive as long as the gate."""
+
+    def __init__(self, num_experts: int, top_k: int, score: str = "softmax", bias=None,
+                 num_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                 renormalize: bool = True, scale: float = 1.0):
+        import torch
+        self._lib = load_library()
+        if score not in SCORES:
+            raise ValueError(f"unknown score {score!r}")
+        if bias is not None:
+            _need(bias, "bias", (num_experts,), (torch.float32,))
+            _on_gpu(None, bias=bias)
+        self.num_experts, self.top_k, self.bias = num_experts, top_k, bias
+        self.desc = GateDesc(ABI_VERSION, num_experts, top_k, SCORES[score], num_groups, topk_groups,
+                             group_top, int(renormalize), scale, _ptr(bias))
+        # the library's own checks of the fields; no tokens, so nothing is enqueued
+        _check(self._lib, self._lib.moe_quant_gate_topk(ctypes.byref(self.desc), None, MQ_F32, 0, None,
+                                                        None, None))
+
+    def topk(self, logits, ids=None, weights=None, stream=None):
+        """The gate of logits [T, E] (float32 or bfloat16): returns (ids int32
+        [T, k], weights float32 [T, k])."""
+        import torch
+        if logits.dim() != 2:
+            raise ValueError("logits must be [T, E]")
+        t, k = logits.shape[0], self.top_k
+        _need(logits, "logits", (t, self.num_experts), (torch.float32, torch.bfloat16))
+        if not _is_current(logits):
+            with torch.cuda.device(logits.device):
+                return self.topk(logits, ids, weights, stream)
+        if ids is None:
+            ids = _empty((t, k), torch.int32, logits.device, stream)
+        if weights is None:
+            weights = _empty((t, k), torch.float32, logits.device, stream)
+        _need(ids, "ids", (t, k), (torch.int32,))
+        _need(weights, "weights", (t, k), (torch.float32,))
+        _on_gpu(logits.device, logits=logits, bias=self.bias, ids=ids, weights=weights)
+        _check(self._lib, self._lib.moe_quant_gate_topk(
+            ctypes.byref(self.desc), _ptr(logits), _mq_dtype(logits.dtype), t, _ptr(ids), _ptr(weights),
+            _stream(stream)))
+        return ids, weights
+
+
+class ResidualNorm:
+    """Norms before and after a block with its gate, the residual scale and the
+    residual add in one pass (moe_quant_norm).
+
+    ``post_weight`` [H]: norm of the block's output (None: none); ``pre_weight``
+    [H]: norm of the new residual, the next block's input (None: none); both
+    float32 or both bfloat16, on the GPU, alive as long as the object.
+    ``weight_offset`` is 1 where weights are stored as w - 1."""
+
+    def __init__(self, hidden: int, post_weight=None, pre_weight=None, eps: float = 1e-6,
+                 weight_offset: float = 0.0, scale: float = 1.0, residual_dtype=None):
+        import torch
+        self._lib = load_library()
+        residual_dtype = residual_dtype or torch.bfloat16
+        types = (torch.float32, torch.bfloat16)
+        if residual_dtype not in types:
+            raise ValueError(f"residual_dtype {residual_dtype}, expected one of {types}")
+        weight_dtype = torch.bfloat16
+        for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+            if w is not None:
+                _need(w, name, (hidden,), types)
+                weight_dtype = w.dtype
+        if post_weight is not None and pre_weight is not None and post_weight.dtype != pre_weight.dtype:
+            raise ValueError("post_weight and pre_weight must have one dtype")
+        _on_gpu(None, post_weight=post_weight, pre_weight=pre_weight)
+        self.hidden, self.residual_dtype = hidden, residual_dtype
+        self.post_weight, self.pre_weight = post_weight, pre_weight
+        self.desc = NormDesc(ABI_VERSION, hidden, _mq_dtype(residual_dtype), _mq_dtype(weight_dtype), eps,
+                             weight_offset, scale, _ptr(post_weight), _ptr(pre_weight))
+        # the library's own checks of the fields; no tokens, so nothing is enqueued
+        _check(self._lib, self._lib.moe_quant_norm(ctypes.byref(self.desc), None, None, None, GATE_NONE, 0, 0,
+                                                   None, None, None))
+
+    def forward(self, x=None, residual=None, gate=None, residual_out=None, norm_out=None, stream=None):
+        """``x`` bfloat16 [T, H] (the block's output), ``residual`` [T, H], ``gate``
+        float32 or bfloat16: [H] per channel, [T, 1] per token or [T, H].
+        Returns (residual_out, norm_out); norm_out is None without a
+        ``pre_weight``.  The outputs may be the inputs' own buffers."""
+        import torch
+        first = x if x is not None else residual
+        if first is None or first.dim() != 2:
+            raise ValueError("need x or residual [T, H]")
+        t, h, dev = first.shape[0], self.hidden, first.device
+        if x is not None:
+            _need(x, "x", (t, h), (torch.bfloat16,))
+        if residual is not None:
+            _need(residual, "residual", (t, h), (self.residual_dtype,))
+        kind = GATE_NONE
+        if gate is not None:
+            shape = tuple(gate.shape)
+            kind = (GATE_CHANNEL if shape == (h,) else GATE_FULL if shape == (t, h)
+                    else GATE_TOKEN if shape == (t, 1) else None)
+            if kind is None:
+                raise ValueError(f"gate has shape {shape}, expected ({h},), ({t}, 1) or ({t}, {h})")
+            _need(gate, "gate", shape, (torch.float32, torch.bfloat16))
+        if not _is_current(first):
+            with torch.cuda.device(dev):
+                return self.forward(x, residual, gate, residual_out, norm_out, stream)
+        if residual_out is None:
+            residual_out = _empty((t, h), self.residual_dtype, dev, stream)
+        _need(residual_out, "residual_out", (t, h), (self.residual_dtype,))
+        if self.pre_weight is None:
+            if norm_out is not None:
+                raise ValueError("norm_out needs a pre_weight")
+        else:
+            if norm_out is None:
+                norm_out = _empty((t, h), torch.bfloat16, dev, stream)
+            _need(norm_out, "norm_out", (t, h), (torch.bfloat16,))
+        _on_gpu(dev, x=x, residual=residual, gate=gate, residual_out=residual_out, norm_out=norm_out,
+                post_weight=self.post_weight, pre_weight=self.pre_weight)
+        _check(self._lib, self._lib.moe_quant_norm(
+            ctypes.byref(self.desc), _ptr(x), _ptr(residual), _ptr(gate), kind,
+            MQ_F32 if gate is None else _mq_dtype(gate.dtype), t, _ptr(residual_out), _ptr(norm_out),
+            _stream(stream)))
+        return residual_out, norm_out
+
+
 class Layer:
     """One MoE expert layer over packed weights resident on the GPU.
 
@@ -404,8 +593,40 @@ class Layer:
         return self._forward(None, router_w, hidden, residual, out, workspace, probe, events,
                              stream, logits_out)
 
+    def forward_gated(self, gate: "Gate", hidden, logits=None, router_w=None, residual=None, out=None,
+                      workspace=None, activations: str = "bf16", act_gscale13: float = 0.0,
+                      act_gscale2: float = 0.0, logits_out=None, probe: Optional[Dict] = None,
+                      events=None, stream=None):
+        """Enqueue one forward under ``gate`` (moe_quant_forward_gated), from router
+        ``logits`` or from the router weight ``router_w`` [E, H]; ``activations``:
+        "bf16", "fp8" (FP8 layers) or "nvfp4" (NVFP4 layers, with the calibrated
+        global scales)."""
+        import torch
+        if (logits is None) == (router_w is None):
+            raise ValueError("forward_gated needs exactly one of logits and router_w")
+        if activations not in ACTIVATIONS:
+            raise ValueError(f"unknown activations {activations!r}")
+        if logits_out is not None and router_w is None:
+            raise ValueError("logits_out needs router_w")
+        if hidden.dim() != 2:
+            raise ValueError("hidden must be [T, H]")
+        if not _is_current(hidden):
+            with torch.cuda.device(hidden.device):
+                return self.forward_gated(gate, hidden, logits, router_w, residual, out, workspace, activations,
+                                          act_gscale13, act_gscale2, logits_out, probe, events, stream)
+        if gate.bias is not None:
+            _on_gpu(self.device, **{"gate.bias": gate.bias})
+        if stream is not None:
+            t = hidden.shape[0]
+            if out is None:
+                out = _empty((t, self.hidden), torch.bfloat16, self.device, stream)
+            if workspace is None:
+                workspace = _empty((max(self.workspace_size(t), 256),), torch.uint8, self.device, stream)
+        return self._forward(logits, router_w, hidden, residual, out, workspace, probe, events, stream, logits_out,
+                             gate=gate, act=(ACTIVATIONS[activations], float(act_gscale13), float(act_gscale2)))
+
     def _forward(self, logits, router_w, hidden, residual, out, workspace, probe, events, stream,
-                 logits_out, w8a8=False, w4a4=None):
+                 logits_out, w8a8=False, w4a4=None, gate=None, act=None):
         import torch
         if hidden.dim() != 2:
             raise ValueError("hidden must be [T, H]")
@@ -454,7 +675,12 @@ class Layer:
                 for i, ev in enumerate(events):
                     pr.events[i] = None if ev is None else ev.cuda_event
         prp = ctypes.byref(pr) if pr is not None else None
-        if router_w is None:
+        if gate is not None:
+            st = self._lib.moe_quant_forward_gated(
+                self._h, ctypes.byref(gate.desc), _ptr(logits), MQ_F32 if logits is None else _mq_dtype(logits.dtype),
+                _ptr(router_w), _ptr(hidden), _ptr(residual), t, _ptr(out), _ptr(workspace), _nbytes(workspace),
+                *act, _ptr(logits_out), prp, _stream(stream))
+        elif router_w is None:
             ldt = MQ_F32 if logits.dtype == torch.float32 else MQ_BF16
             if w4a4 is not None:
                 st = self._lib.moe_quant_forward_w4a4(

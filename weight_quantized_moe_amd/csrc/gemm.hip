@@ -1368,13 +1368,14 @@ __global__ __launch_bounds__(512) void gemm_decode_down_tok(GemmArgs a) {
 // larger than the 256 MiB last-level cache (NVFP4 Zipf T=16384, 537 MB:
 // 107 -> 88 us); a smaller one is still partly cached from the down GEMM's
 // writes, and plain loads read it faster (FP8 T=4096, 134 MB: 23.5 against
-// 24.7 us).
+// 24.7 us).  kScaled: the sum times wscale[t], the power of two that gated
+// routing takes out of a token's weights.
 // ===========================================================================
-template <bool kStream>
+template <bool kStream, bool kScaled>
 __global__ __launch_bounds__(256) void combine_kernel(const _Float16 *__restrict__ partial,
                                                       const uint16_t *__restrict__ residual,
                                                       uint16_t *__restrict__ out, int T, int H,
-                                                      int k) {
+                                                      int k, const float *__restrict__ wscale) {
   const int per_row = H / 8;
   const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= (size_t)T * per_row) return;
@@ -1397,6 +1398,11 @@ __global__ __launch_bounds__(256) void combine_kernel(const _Float16 *__restrict
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += (float)x[jj][i];
       }
+  }
+  if (kScaled) {
+    const float ws = wscale[t];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= ws;
   }
   if (residual) {
     const u4 rv = *(const u4 *)(residual + (size_t)t * H + c);
@@ -1738,10 +1744,10 @@ hipError_t launch_combine(const LayerDims &L, const FwdPtrs &P, const Workspace 
   const bool stream = (size_t)P.T * L.k * L.H * sizeof(_Float16) > ((size_t)256 << 20);
   const dim3 grid((unsigned)((items + 255) / 256)), block(256);
   const _Float16 *partial = (const _Float16 *)(P.ws + W.partial);
-  if (stream)
-    hipLaunchKernelGGL(combine_kernel<true>, grid, block, 0, s, partial, P.residual, P.out, P.T, L.H, L.k);
-  else
-    hipLaunchKernelGGL(combine_kernel<false>, grid, block, 0, s, partial, P.residual, P.out, P.T, L.H, L.k);
+  const float *ws = P.gated ? (const float *)(P.ws + W.wscale) : nullptr;
+  auto f = stream ? (ws ? combine_kernel<true, true> : combine_kernel<true, false>)
+                  : (ws ? combine_kernel<false, true> : combine_kernel<false, false>);
+  hipLaunchKernelGGL(f, grid, block, 0, s, partial, P.residual, P.out, P.T, L.H, L.k, ws);
   return hipGetLastError();
 }
 

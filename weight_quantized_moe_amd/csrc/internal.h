@@ -75,6 +75,7 @@ struct Workspace {
   size_t h;                    // fp16 [R, I]
   size_t partial;              // fp16 [R, H]: routing-weighted expert outputs per slot
   size_t chunks;               // int32 [kMaxChunks, E]: per-chunk expert counts, then bases
+  size_t wscale;               // float [T]: gated routing, the power of two taken out of a token's weights
   size_t flags;                // uint32 [4] at offset 0: bit 0 = an FP16 intermediate saturated
   size_t total;
 };
@@ -88,7 +89,10 @@ struct LayerDims {
   const float *g13, *g2;
 };
 
+struct GateArgs;
+
 struct FwdPtrs {
+  const GateArgs *gated;   // gated routing (null: softmax over the k largest logits)
   const void *logits;
   int logits_bf16;
   const uint16_t *gate_w;  // BF16 router weight [E, H]: logits computed in-library (else null)
@@ -147,6 +151,40 @@ hipError_t launch_w8a8_down(const LayerDims &L, const FwdPtrs &P, const Workspac
 hipError_t launch_router_logits(const uint16_t *x, const uint16_t *w, float *out, int64_t T, int H,
                                 int E, hipStream_t s);
 
+// The gate's parameters as its kernels take them (group_top is 1 without groups).
+constexpr int kMaxGateGroups = 64;
+struct GateArgs {
+  int E, k, groups, per, topk_groups, group_top, score, renormalize;
+  float scale;
+  const float *bias;  // [E] or null
+};
+// Where the gate's results go.  wscale (nullable): a power of two per token is
+// taken out of wts, which then lie in [2^-1, 1) at their largest, and written
+// there (the expert layer rounds its per-slot products to FP16).  p_ids and p_w
+// (nullable): copies with the weights themselves.
+struct GateOut {
+  int32_t *ids;
+  float *wts, *wscale;
+  int32_t *p_ids;
+  float *p_w;
+};
+hipError_t launch_gate_topk(const GateArgs &g, const void *logits, int bf16, int64_t T, const GateOut &o,
+                            hipStream_t s);
+// Routing stage of a gated forward: the gate, then the hidden rows' staging.
+hipError_t launch_route_gated(const LayerDims &L, const FwdPtrs &P, const Workspace &W, bool decode, int stage_rows,
+                              hipStream_t s);
+
+constexpr int kMaxNormHidden = 32768;
+struct NormArgs {
+  const uint16_t *x;
+  const void *residual, *gate, *post_w, *pre_w;
+  void *residual_out;
+  uint16_t *norm_out;
+  int H, r_bf16, w_bf16, gate_kind, gate_bf16;
+  float eps, offset, scale;
+};
+hipError_t launch_norm(const NormArgs &a, int64_t T, hipStream_t s);
+
 // The forward path behind moe_quant_forward and its allocation-free variant:
 // host checks, then the launch sequence on `stream`.  `flags` (nullable) is
 // the saturation word to use instead of the workspace's first word.
@@ -156,7 +194,7 @@ mq_status forward_impl(const mq_layer *L, const void *router_logits, int32_t log
                        size_t workspace_bytes, const mq_probe *probe, uint32_t *flags,
                        hipStream_t stream, const uint16_t *gate_w = nullptr,
                        float *logits_out = nullptr, int w8a8 = 0, float act_g13 = 0.f,
-                       float act_g2 = 0.f);
+                       float act_g2 = 0.f, const GateArgs *gated = nullptr);
 // Record a status and its one-line explanation for moe_quant_last_error().
 mq_status fail(mq_status s, const char *fmt, ...);
 void clear_error();

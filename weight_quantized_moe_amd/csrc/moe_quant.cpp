@@ -62,6 +62,7 @@ Workspace workspace_layout(int64_t T, int E, int H, int I, int k) {
   w.logits = take((size_t)T * E * 4);
   w.h = take(R * (size_t)I * 2);
   w.partial = take(R * (size_t)H * 2);
+  w.wscale = take((size_t)T * 4);
   w.total = o;
   return w;
 }
@@ -180,14 +181,14 @@ mq_status mq::forward_impl(const mq_layer *L, const void *router_logits, int32_t
                            int64_t num_tokens, uint16_t *out_bf16, void *workspace,
                            size_t workspace_bytes, const mq_probe *probe, uint32_t *flags,
                            hipStream_t stream, const uint16_t *gate_w, float *logits_out,
-                           int w8a8, float act_g13, float act_g2) {
+                           int w8a8, float act_g13, float act_g2, const GateArgs *gated) {
   if (!L) return fail(MQ_E_NULL, "forward: NULL layer handle");
   if (num_tokens < 0 || num_tokens > kMaxTokens)
     return fail(MQ_E_SHAPE, "forward: num_tokens %lld outside [0, %lld]", (long long)num_tokens,
                 (long long)kMaxTokens);
   if (!gate_w && logits_dtype != MQ_F32 && logits_dtype != MQ_BF16)
     return fail(MQ_E_DTYPE, "forward: unknown logits dtype %d", logits_dtype);
-  if (gate_w && L->d.num_experts > mq::kMaxGateExperts)
+  if (gate_w && !gated && L->d.num_experts > mq::kMaxGateExperts)
     return fail(MQ_E_SHAPE, "forward_with_router: %d experts, the fused router holds at most %d",
                 L->d.num_experts, mq::kMaxGateExperts);
   if (num_tokens == 0) {
@@ -214,6 +215,7 @@ mq_status mq::forward_impl(const mq_layer *L, const void *router_logits, int32_t
   }
 
   mq::FwdPtrs P{};
+  P.gated = gated;
   P.logits = router_logits;
   P.logits_bf16 = logits_dtype == MQ_BF16;
   P.gate_w = gate_w;
@@ -361,6 +363,151 @@ mq_status moe_quant_forward_with_router(const mq_layer *L, const uint16_t *hidde
   return mq::forward_impl(L, nullptr, MQ_F32, hidden_bf16, residual_bf16, num_tokens, out_bf16,
                           workspace, workspace_bytes, probe, nullptr, (hipStream_t)stream,
                           router_bf16, logits_out);
+}
+
+static mq_status check_gate(const mq_gate *g, const char *who) {
+  if (g->abi_version != MOE_QUANT_ABI_VERSION)
+    return fail(MQ_E_ABI, "%s: gate abi_version %u, library %u", who, g->abi_version, MOE_QUANT_ABI_VERSION);
+  const int E = g->num_experts, k = g->top_k, G = g->num_groups;
+  if (E < 1 || E > mq::kMaxExperts)
+    return fail(MQ_E_SHAPE, "%s: num_experts %d outside [1, %d]", who, E, mq::kMaxExperts);
+  if (g->score != MQ_SCORE_SOFTMAX && g->score != MQ_SCORE_SIGMOID)
+    return fail(MQ_E_SHAPE, "%s: unknown score %d", who, g->score);
+  if (G < 1 || G > mq::kMaxGateGroups || E % G)
+    return fail(MQ_E_SHAPE, "%s: num_groups %d must divide num_experts %d and be at most %d", who, G, E,
+                mq::kMaxGateGroups);
+  if (g->topk_groups < 1 || g->topk_groups > G)
+    return fail(MQ_E_SHAPE, "%s: topk_groups %d outside [1, %d]", who, g->topk_groups, G);
+  if ((g->group_top != 1 && g->group_top != 2) || (G > 1 && g->group_top > E / G))
+    return fail(MQ_E_SHAPE, "%s: group_top %d must be 1 or 2, and at most the %d experts of a group", who,
+                g->group_top, E / G);
+  if (k < 1 || k > 64 || k > g->topk_groups * (E / G))
+    return fail(MQ_E_SHAPE, "%s: top_k %d outside [1, min(64, %d experts of the kept groups)]", who, k,
+                g->topk_groups * (E / G));
+  if (!std::isfinite(g->scale)) return fail(MQ_E_SHAPE, "%s: scale %g must be finite", who, (double)g->scale);
+  if (g->bias && !aligned(g->bias, 4)) return fail(MQ_E_ALIGN, "%s: bias must be 4-byte aligned", who);
+  return MQ_OK;
+}
+
+static mq::GateArgs gate_args(const mq_gate *g) {
+  mq::GateArgs a;
+  a.E = g->num_experts; a.k = g->top_k; a.groups = g->num_groups; a.per = g->num_experts / g->num_groups;
+  a.topk_groups = g->topk_groups; a.group_top = g->num_groups > 1 ? g->group_top : 1;
+  a.score = g->score; a.renormalize = g->renormalize != 0; a.scale = g->scale; a.bias = g->bias;
+  return a;
+}
+
+mq_status moe_quant_gate_topk(const mq_gate *g, const void *logits, int32_t logits_dtype,
+                              int64_t num_tokens, int32_t *ids, float *weights,
+                              struct ihipStream_t *stream) {
+  if (!g) return fail(MQ_E_NULL, "gate_topk: NULL gate");
+  const mq_status st = check_gate(g, "gate_topk");
+  if (st != MQ_OK) return st;
+  if (num_tokens < 0 || num_tokens > kMaxTokens)
+    return fail(MQ_E_SHAPE, "gate_topk: num_tokens %lld outside [0, %lld]", (long long)num_tokens,
+                (long long)kMaxTokens);
+  if (logits_dtype != MQ_F32 && logits_dtype != MQ_BF16)
+    return fail(MQ_E_DTYPE, "gate_topk: unknown logits dtype %d", logits_dtype);
+  if (num_tokens == 0) {
+    g_err[0] = 0;
+    return MQ_OK;
+  }
+  if (!logits || !ids || !weights) return fail(MQ_E_NULL, "gate_topk: logits, ids and weights must be non-NULL");
+  if (!aligned(logits, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(MQ_E_ALIGN, "gate_topk: logits 16-byte, ids and weights 4-byte aligned");
+  const hipError_t e = mq::launch_gate_topk(gate_args(g), logits, logits_dtype == MQ_BF16, num_tokens,
+                                            {ids, weights, nullptr, nullptr, nullptr}, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(MQ_E_HIP, "gate_topk: %s", hipGetErrorString(e));
+  g_err[0] = 0;
+  return MQ_OK;
+}
+
+mq_status moe_quant_forward_gated(const mq_layer *L, const mq_gate *gate, const void *router_logits,
+                                  int32_t logits_dtype, const uint16_t *router_bf16,
+                                  const uint16_t *hidden_bf16, const uint16_t *residual_bf16,
+                                  int64_t num_tokens, uint16_t *out_bf16, void *workspace,
+                                  size_t workspace_bytes, int32_t activations, float act_gscale13,
+                                  float act_gscale2, float *logits_out, const mq_probe *probe,
+                                  struct ihipStream_t *stream) {
+  if (!L || !gate) return fail(MQ_E_NULL, "forward_gated: NULL layer handle or gate");
+  const mq_status st = check_gate(gate, "forward_gated");
+  if (st != MQ_OK) return st;
+  if (gate->num_experts != L->d.num_experts || gate->top_k != L->d.top_k)
+    return fail(MQ_E_SHAPE, "forward_gated: the gate picks %d of %d experts, the layer %d of %d", gate->top_k,
+                gate->num_experts, L->d.top_k, L->d.num_experts);
+  if (num_tokens != 0 && (router_logits != nullptr) == (router_bf16 != nullptr))
+    return fail(MQ_E_NULL, "forward_gated: exactly one of logits and router weight must be given");
+  if (logits_out && !router_bf16)
+    return fail(MQ_E_NULL, "forward_gated: logits_out needs the router weight");
+  if (activations != MQ_ACT_BF16 && activations != MQ_ACT_FP8 && activations != MQ_ACT_NVFP4)
+    return fail(MQ_E_FORMAT, "forward_gated: unknown activations %d", activations);
+  if (activations == MQ_ACT_FP8 && L->d.format != MQ_W_FP8_B128)
+    return fail(MQ_E_FORMAT, "forward_gated: FP8 activations apply to MQ_W_FP8_B128 layers (format %d)", L->d.format);
+  if (activations == MQ_ACT_NVFP4) {
+    if (L->d.format != MQ_W_NVFP4_G16)
+      return fail(MQ_E_FORMAT, "forward_gated: NVFP4 activations apply to MQ_W_NVFP4_G16 layers (format %d)",
+                  L->d.format);
+    if (!valid_gscale(act_gscale13) || !valid_gscale(act_gscale2))
+      return fail(MQ_E_SHAPE, "forward_gated: activation global scales %g and %g must be finite and positive",
+                  (double)act_gscale13, (double)act_gscale2);
+  }
+  const mq::GateArgs g = gate_args(gate);
+  const bool nvfp4 = activations == MQ_ACT_NVFP4;
+  return mq::forward_impl(L, router_logits, logits_dtype, hidden_bf16, residual_bf16, num_tokens, out_bf16,
+                          workspace, workspace_bytes, probe, nullptr, (hipStream_t)stream, router_bf16, logits_out,
+                          activations == MQ_ACT_FP8, nvfp4 ? act_gscale13 : 0.f, nvfp4 ? act_gscale2 : 0.f, &g);
+}
+
+static bool known_dtype(int32_t d) { return d == MQ_F32 || d == MQ_BF16; }
+
+mq_status moe_quant_norm(const mq_norm *n, const uint16_t *x_bf16, const void *residual,
+                         const void *gate, int32_t gate_kind, int32_t gate_dtype, int64_t num_tokens,
+                         void *residual_out, uint16_t *norm_out_bf16, struct ihipStream_t *stream) {
+  if (!n) return fail(MQ_E_NULL, "norm: NULL descriptor");
+  if (n->abi_version != MOE_QUANT_ABI_VERSION)
+    return fail(MQ_E_ABI, "norm: descriptor abi_version %u, library %u", n->abi_version, MOE_QUANT_ABI_VERSION);
+  if (n->hidden < 1 || n->hidden > mq::kMaxNormHidden)
+    return fail(MQ_E_SHAPE, "norm: hidden %d outside [1, %d]", n->hidden, mq::kMaxNormHidden);
+  if (!known_dtype(n->residual_dtype) || !known_dtype(n->weight_dtype) ||
+      (gate_kind != MQ_GATE_NONE && !known_dtype(gate_dtype)))
+    return fail(MQ_E_DTYPE, "norm: unknown residual, weight or gate dtype (%d, %d, %d)", n->residual_dtype,
+                n->weight_dtype, gate_dtype);
+  if (!std::isfinite(n->eps) || !(n->eps > 0.f))
+    return fail(MQ_E_SHAPE, "norm: eps %g must be finite and positive", (double)n->eps);
+  if (!std::isfinite(n->weight_offset) || !std::isfinite(n->scale))
+    return fail(MQ_E_SHAPE, "norm: weight_offset %g and scale %g must be finite", (double)n->weight_offset,
+                (double)n->scale);
+  if (gate_kind < MQ_GATE_NONE || gate_kind > MQ_GATE_FULL)
+    return fail(MQ_E_SHAPE, "norm: unknown gate kind %d", gate_kind);
+  if (num_tokens < 0 || num_tokens > kMaxTokens)
+    return fail(MQ_E_SHAPE, "norm: num_tokens %lld outside [0, %lld]", (long long)num_tokens, (long long)kMaxTokens);
+  if (num_tokens == 0) {
+    g_err[0] = 0;
+    return MQ_OK;
+  }
+  if ((gate != nullptr) != (gate_kind != MQ_GATE_NONE))
+    return fail(MQ_E_NULL, "norm: gate must be given exactly for a gate kind other than MQ_GATE_NONE");
+  if (!x_bf16 && (n->post_weight || gate))
+    return fail(MQ_E_NULL, "norm: post_weight and gate apply to x, which is NULL");
+  if (!x_bf16 && !residual) return fail(MQ_E_NULL, "norm: x and residual are both NULL");
+  if ((n->pre_weight != nullptr) != (norm_out_bf16 != nullptr))
+    return fail(MQ_E_NULL, "norm: norm_out must be given exactly when pre_weight is");
+  if (!residual_out && !norm_out_bf16) return fail(MQ_E_NULL, "norm: no output is wanted");
+  for (const void *p : {(const void *)x_bf16, residual, (const void *)residual_out, (const void *)norm_out_bf16,
+                        n->post_weight, n->pre_weight, gate_kind == MQ_GATE_TOKEN ? nullptr : gate})
+    if (p && !aligned(p, 16)) return fail(MQ_E_ALIGN, "norm: arrays must be 16-byte aligned");
+  if (gate && !aligned(gate, gate_dtype == MQ_F32 ? 4 : 2))
+    return fail(MQ_E_ALIGN, "norm: a per-token gate must be aligned to its element");
+  mq::NormArgs a;
+  a.x = x_bf16; a.residual = residual; a.gate = gate; a.post_w = n->post_weight; a.pre_w = n->pre_weight;
+  a.residual_out = residual_out; a.norm_out = norm_out_bf16;
+  a.H = n->hidden; a.r_bf16 = n->residual_dtype == MQ_BF16; a.w_bf16 = n->weight_dtype == MQ_BF16;
+  a.gate_kind = gate_kind; a.gate_bf16 = gate_dtype == MQ_BF16;
+  a.eps = n->eps; a.offset = n->weight_offset; a.scale = n->scale;
+  const hipError_t e = mq::launch_norm(a, num_tokens, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(MQ_E_HIP, "norm: %s", hipGetErrorString(e));
+  g_err[0] = 0;
+  return MQ_OK;
 }
 
 mq_status moe_quant_import_expert(const mq_layer_desc *dst, int32_t expert, const mq_src_proj *gate,

@@ -529,6 +529,7 @@ hipError_t launch_route(const LayerDims &L, const FwdPtrs &P, const Workspace &W
   // larger decode rows: the GEMM finds the scales too (0); W8A8: FP8 codes
   // and scales (3); W4A4: NVFP4 values and 1 / g (4)
   const int stage_rows = P.w8a8 ? 3 : P.act_g13 > 0.f ? 4 : !decode ? 1 : L.H <= kRowRegsMaxH ? 2 : 0;
+  if (P.gated) return launch_route_gated(L, P, W, decode, stage_rows, s);
   if (P.gate_w && P.T >= kGateFusedMinT)  // router GEMM fused with the top-k
     return L.fmt == FMT_INT4 ? gate_route_dispatch<true>(L, P, W, stage_rows, s)
                              : gate_route_dispatch<false>(L, P, W, stage_rows, s);
@@ -555,7 +556,7 @@ hipError_t launch_route(const LayerDims &L, const FwdPtrs &P, const Workspace &W
 
 bool route_groups(const LayerDims &L, const FwdPtrs &P, bool decode) {
   (void)L;
-  return decode && !P.w8a8 && P.act_g13 == 0.f && P.T <= kFusedT;
+  return !P.gated && decode && !P.w8a8 && P.act_g13 == 0.f && P.T <= kFusedT;
 }
 
 hipError_t launch_permute(const LayerDims &L, const FwdPtrs &P, const Workspace &W, bool decode,
