@@ -3,8 +3,13 @@
 //   z  = x  or  x rsqrt(mean x^2 + eps) (offset + w_post)
 //   r' = round(residual + scale gate z)
 //   n  = bf16(r' rsqrt(mean r'^2 + eps) (offset + w_pre))
-// One workgroup per row keeps the row in LDS in 32 bits between the steps, so
-// every input is read once and every output written once.
+// A row is held in the registers of one wave or of one workgroup in 32 bits
+// between the steps: every input is read once, every output written once, and
+// the kernel is bound by those bytes.  Lane c of NT holds values
+// 8 (c + NT j) + [0, 8), j < R, so loads and stores are 16 bytes per lane and
+// consecutive over the lanes.  Rows whose length is no multiple of 8 start at
+// odd addresses: the same loads, which the hardware takes at any alignment of
+// the element, with single values in the last lane.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -14,67 +19,221 @@
 
 namespace mq {
 
-__device__ __forceinline__ float load_as_f32(const void *p, int bf16, int64_t i) {
-  return bf16 ? bf16_to_f32(((const uint16_t *)p)[i]) : ((const float *)p)[i];
+typedef u4 u4_a2 __attribute__((aligned(2)));
+typedef u4 u4_a4 __attribute__((aligned(4)));
+typedef f4 f4_a4 __attribute__((aligned(4)));
+
+struct Row8 {
+  float v[8];
+};
+// 8 values as they lie in memory: 8 BF16 values in a, or 8 floats in a and b.
+// Loads keep this form until the values are used, so that none of them is
+// waited for at the branch that picked its type.
+struct Raw8 {
+  u4 a, b;
+};
+
+__device__ __forceinline__ Row8 widen(u4 u) {
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.v[2 * i] = bf16_to_f32(u[i] & 0xFFFFu);
+    r.v[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
+  }
+  return r;
+}
+__device__ __forceinline__ Row8 widen(const Raw8 &w, int bf16) {
+  if (bf16) return widen(w.a);
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.v[i] = __builtin_bit_cast(float, (uint32_t)w.a[i]);
+    r.v[4 + i] = __builtin_bit_cast(float, (uint32_t)w.b[i]);
+  }
+  return r;
 }
 
-// Sum of v over a workgroup of `waves` waves, in a fixed order; red: LDS floats.
-__device__ __forceinline__ float block_sum(float v, float *red, int waves) {
-  v = sum64f(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < waves; ++w) s += red[w];
-  return s;
+// 8 values of p's row from index at on, in a row of n (0 from its end on).
+template <bool kTail>
+__device__ __forceinline__ Raw8 load8(const void *p, int bf16, int64_t row, int at, int n) {
+  Raw8 w = {u4{0u, 0u, 0u, 0u}, u4{0u, 0u, 0u, 0u}};
+  if (bf16) {
+    const uint16_t *q = (const uint16_t *)p + row + at;
+    if (at + 8 <= n) {
+      w.a = *(const u4_a2 *)q;
+    } else if (kTail) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (at + i < n) w.a[i >> 1] |= (uint32_t)q[i] << (16 * (i & 1));
+    }
+  } else {
+    const uint32_t *q = (const uint32_t *)p + row + at;
+    if (at + 8 <= n) {
+      w.a = *(const u4_a4 *)q;
+      w.b = *(const u4_a4 *)(q + 4);
+    } else if (kTail) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (at + i < n) (i < 4 ? w.a : w.b)[i & 3] = q[i];
+    }
+  }
+  return w;
+}
+template <bool kTail>
+__device__ __forceinline__ void store_bf16x8(uint16_t *p, int at, int n, u4 u) {
+  if (at + 8 <= n) {
+    *(u4_a2 *)(p + at) = u;
+  } else if (kTail) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (at + i < n) p[at + i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+  }
+}
+template <bool kTail>
+__device__ __forceinline__ void store_f32x8(float *p, int at, int n, const Row8 &r) {
+  if (at + 8 <= n) {
+    *(f4_a4 *)(p + at) = f4{r.v[0], r.v[1], r.v[2], r.v[3]};
+    *(f4_a4 *)(p + at + 4) = f4{r.v[4], r.v[5], r.v[6], r.v[7]};
+  } else if (kTail) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (at + i < n) p[at + i] = r.v[i];
+  }
+}
+__device__ __forceinline__ u4 narrow(const Row8 &r) {
+  u4 u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    u[i] = (uint32_t)f32_to_bf16_rne(r.v[2 * i]) | ((uint32_t)f32_to_bf16_rne(r.v[2 * i + 1]) << 16);
+  return u;
 }
 
-__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
-  extern __shared__ __align__(16) float row[];  // [H]
-  __shared__ float red[4];
-  const int H = a.H, tid = threadIdx.x;
-  const int64_t t = blockIdx.x, o = t * H;
+// 1 / sqrt(mean + eps) of a row whose lanes hold partial sums ss of squares;
+// over several waves the sums are added in wave order (red: 16 floats of LDS).
+template <bool kOneWave>
+__device__ __forceinline__ float inv_rms(float ss, int H, float eps, float *red) {
+  ss = sum64f(ss);
+  if (!kOneWave) {
+    const int waves = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ss;
+    __syncthreads();
+    ss = red[0];
+    for (int w = 1; w < waves; ++w) ss += red[w];
+  }
+  return 1.f / sqrtf(ss / H + eps);
+}
+
+// kOneWave: four rows per workgroup, one per wave; else one row per workgroup.
+template <int R, bool kOneWave, bool kResBf16, bool kTail>
+__global__ __launch_bounds__(kOneWave ? 256 : 1024) void norm_kernel(NormArgs a, int64_t T) {
+  constexpr bool kEarly = R <= 2;  // 4 x 40 values a lane would not fit its registers
+  __shared__ float red[2][16];
+  const int H = a.H, NT = kOneWave ? 64 : blockDim.x;
+  const int c = kOneWave ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t t = kOneWave ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (t >= T) return;  // whole waves, and no barrier follows for them
+  const int64_t o = t * H;
+  const bool vec_gate = a.gate_kind == MQ_GATE_CHANNEL || a.gate_kind == MQ_GATE_FULL;
+  const int64_t go = a.gate_kind == MQ_GATE_FULL ? o : 0;
+  Raw8 x[R] = {}, res[R] = {}, g[R], w_post[R], w_pre[R];
+  if (a.x) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) x[j] = load8<kTail>(a.x, 1, o, 8 * (c + NT * j), H);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) res[j] = load8<kTail>(a.residual, kResBf16, o, 8 * (c + NT * j), H);
+  }
+  // everything the row needs is on its way before the first sum is taken
+  auto load_gate = [&](int j) { g[j] = load8<kTail>(a.gate, a.gate_bf16, go, 8 * (c + NT * j), H); };
+  auto load_post = [&](int j) { w_post[j] = load8<kTail>(a.post_w, a.w_bf16, 0, 8 * (c + NT * j), H); };
+  auto load_pre = [&](int j) { w_pre[j] = load8<kTail>(a.pre_w, a.w_bf16, 0, 8 * (c + NT * j), H); };
+  if (kEarly) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (vec_gate) load_gate(j);
+      if (a.post_w) load_post(j);
+      if (a.pre_w) load_pre(j);
+    }
+  }
+  float scale = a.scale;
+  if (a.gate_kind == MQ_GATE_TOKEN)
+    scale *= a.gate_bf16 ? bf16_to_f32(((const uint16_t *)a.gate)[t]) : ((const float *)a.gate)[t];
+  Row8 v[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) v[j] = widen(x[j].a);
   float ss = 0.f;
-  if (a.x)
-    for (int i = tid; i < H; i += 256) {
-      const float v = bf16_to_f32(a.x[o + i]);
-      row[i] = v;
-      ss += v * v;
+  if (a.post_w) {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += v[j].v[i] * v[j].v[i];
+    const float inv = inv_rms<kOneWave>(ss, H, a.eps, red[0]);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (!kEarly) load_post(j);
+      const Row8 w = widen(w_post[j], a.w_bf16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j].v[i] *= inv * (a.offset + w.v[i]);
     }
-  float inv = 1.f;
-  if (a.post_w) inv = 1.f / sqrtf(block_sum(ss, red, 4) / H + a.eps);
+  }
+  if (vec_gate) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (!kEarly) load_gate(j);
+      const Row8 w = widen(g[j], a.gate_bf16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j].v[i] *= w.v[i];
+    }
+  }
   ss = 0.f;
-  for (int i = tid; i < H; i += 256) {
-    float v = 0.f;
-    if (a.x) {
-      v = row[i];
-      if (a.post_w) v = v * inv * (a.offset + load_as_f32(a.post_w, a.w_bf16, i));
-      if (a.gate_kind == MQ_GATE_CHANNEL) v *= load_as_f32(a.gate, a.gate_bf16, i);
-      if (a.gate_kind == MQ_GATE_TOKEN) v *= load_as_f32(a.gate, a.gate_bf16, t);
-      if (a.gate_kind == MQ_GATE_FULL) v *= load_as_f32(a.gate, a.gate_bf16, o + i);
-      v *= a.scale;
-    }
-    if (a.residual) v = load_as_f32(a.residual, a.r_bf16, o + i) + v;
-    if (a.r_bf16) {
-      const uint16_t b = f32_to_bf16_rne(v);
-      if (a.residual_out) ((uint16_t *)a.residual_out)[o + i] = b;
-      v = bf16_to_f32(b);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const Row8 r = widen(res[j], kResBf16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j].v[i] = r.v[i] + scale * v[j].v[i];
+    if (kResBf16) {
+      const u4 u = narrow(v[j]);
+      if (a.residual_out) store_bf16x8<kTail>((uint16_t *)a.residual_out + o, 8 * (c + NT * j), H, u);
+      v[j] = widen(u);
     } else if (a.residual_out) {
-      ((float *)a.residual_out)[o + i] = v;
+      store_f32x8<kTail>((float *)a.residual_out + o, 8 * (c + NT * j), H, v[j]);
     }
-    row[i] = v;
-    ss += v * v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += v[j].v[i] * v[j].v[i];
   }
   if (!a.norm_out) return;
-  inv = 1.f / sqrtf(block_sum(ss, red, 4) / H + a.eps);
-  for (int i = tid; i < H; i += 256)
-    a.norm_out[o + i] = f32_to_bf16_rne(row[i] * inv * (a.offset + load_as_f32(a.pre_w, a.w_bf16, i)));
+  const float inv = inv_rms<kOneWave>(ss, H, a.eps, red[1]);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    if (!kEarly) load_pre(j);
+    const Row8 w = widen(w_pre[j], a.w_bf16);
+    Row8 n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n.v[i] = v[j].v[i] * inv * (a.offset + w.v[i]);
+    store_bf16x8<kTail>(a.norm_out + o, 8 * (c + NT * j), H, narrow(n));
+  }
+}
+
+template <int R, bool kOneWave>
+static void norm_launch(const NormArgs &a, int64_t T, int threads, hipStream_t s) {
+  const bool tail = a.H % 8 != 0;
+  auto f = a.r_bf16 ? (tail ? norm_kernel<R, kOneWave, true, true> : norm_kernel<R, kOneWave, true, false>)
+                    : (tail ? norm_kernel<R, kOneWave, false, true> : norm_kernel<R, kOneWave, false, false>);
+  const dim3 grid((unsigned)(kOneWave ? (T + 3) / 4 : T));
+  hipLaunchKernelGGL(f, grid, dim3(threads), 0, s, a, T);
 }
 
 hipError_t launch_norm(const NormArgs &a, int64_t T, hipStream_t s) {
-  const size_t lds = (size_t)a.H * 4;
-  if (lds > 48 * 1024) raise_lds_limit((const void *)norm_kernel);
-  hipLaunchKernelGGL(norm_kernel, dim3((unsigned)T), dim3(256), lds, s, a);
+  const int eights = (a.H + 7) / 8;
+  if (eights <= 64)
+    norm_launch<1, true>(a, T, 256, s);
+  else if (eights <= 1024)
+    norm_launch<1, false>(a, T, (eights + 63) / 64 * 64, s);
+  else if (eights <= 2048)
+    norm_launch<2, false>(a, T, 1024, s);
+  else
+    norm_launch<4, false>(a, T, 1024, s);
   return hipGetLastError();
 }
 
