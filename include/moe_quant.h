@@ -362,7 +362,8 @@ mq_status moe_quant_router_logits(const uint16_t *hidden_bf16, const uint16_t *r
  * Masked experts: an expert whose logit or bias is -inf or NaN has c = -inf and
  * weight 0.  It is selected only where fewer than k experts of the kept groups
  * are left, lower ids first; a row without any live expert has weights 0 and k
- * distinct valid ids.  A logit of +inf counts as the largest finite float.
+ * distinct valid ids.  A logit or bias of +inf counts as the largest finite
+ * float.
  */
 typedef enum { MQ_SCORE_SOFTMAX = 0, MQ_SCORE_SIGMOID = 1 } mq_score;
 

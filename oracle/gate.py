@@ -43,7 +43,7 @@ def gate(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_t
         c = list(s)
         if bias is not None:
             for i in range(e):
-                b = float(bias[i])
+                b = min(float(bias[i]), biggest)
                 live[i] = live[i] and b > -math.inf          # False for NaN too
                 c[i] = s[i] + b
         # without a bias the scores' order is the logits' own

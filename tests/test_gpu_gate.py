@@ -158,7 +158,7 @@ def test_masks(kind, dtype, groups, topk_groups):
     lg[10] = torch.finfo(dtype).max
     lg[11, : e // 3] = -inf
     bias = a_bias(e)
-    bias[4], bias[21] = -inf, math.nan
+    bias[4], bias[21], bias[33] = -inf, math.nan, inf
     for b in (None, bias):
         check(lg, k, bias=b, groups=groups, topk_groups=topk_groups, group_top=2 if groups > 1 else 1, **KINDS[kind])
 

@@ -230,11 +230,19 @@ def _on_gpu(device, **tensors):
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _is_current(t) -> bool:
-    """Whether ``t`` is on the current GPU (a tensor elsewhere than on a GPU is
-    left to _on_gpu)."""
+def _fits(t, shape, dtype, index) -> bool:
+    """Whether ``t`` is a contiguous tensor of this shape and dtype on GPU ``index``:
+    the checks of _need and _on_gpu in the form that costs the least, in front of
+    them (they name what is wrong).  Small calls are bound by the host."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
+
+
+def _raw_stream(stream, index) -> Optional[int]:
+    """The HIP stream of ``stream``, or of GPU ``index``'s current one."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    return not t.is_cuda or t.device.index == torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -388,10 +396,13 @@ class Gate:
             _need(bias, "bias", (num_experts,), (torch.float32,))
             _on_gpu(None, bias=bias)
         self.num_experts, self.top_k, self.bias = num_experts, top_k, bias
+        self._f32, self._bf16, self._i32 = torch.float32, torch.bfloat16, torch.int32
+        self._bias_index = None if bias is None else bias.get_device()
         self.desc = GateDesc(ABI_VERSION, num_experts, top_k, SCORES[score], num_groups, topk_groups,
                              group_top, int(renormalize), scale, _ptr(bias))
+        self._ref = ctypes.byref(self.desc)
         # the library's own checks of the fields; no tokens, so nothing is enqueued
-        _check(self._lib, self._lib.moe_quant_gate_topk(ctypes.byref(self.desc), None, MQ_F32, 0, None,
+        _check(self._lib, self._lib.moe_quant_gate_topk(self._ref, None, MQ_F32, 0, None,
                                                         None, None))
 
     def topk(self, logits, ids=None, weights=None, stream=None):
@@ -400,21 +411,27 @@ class Gate:
         import torch
         if logits.dim() != 2:
             raise ValueError("logits must be [T, E]")
-        t, k = logits.shape[0], self.top_k
-        _need(logits, "logits", (t, self.num_experts), (torch.float32, torch.bfloat16))
-        if not _is_current(logits):
-            with torch.cuda.device(logits.device):
+        t, k, index, dtype = logits.shape[0], self.top_k, logits.get_device(), logits.dtype
+        bf16 = dtype is self._bf16
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return self.topk(logits, ids, weights, stream)
+        shape = (t, k)
         if ids is None:
-            ids = _empty((t, k), torch.int32, logits.device, stream)
+            ids = _empty(shape, torch.int32, logits.device, stream)
         if weights is None:
-            weights = _empty((t, k), torch.float32, logits.device, stream)
-        _need(ids, "ids", (t, k), (torch.int32,))
-        _need(weights, "weights", (t, k), (torch.float32,))
-        _on_gpu(logits.device, logits=logits, bias=self.bias, ids=ids, weights=weights)
-        _check(self._lib, self._lib.moe_quant_gate_topk(
-            ctypes.byref(self.desc), _ptr(logits), _mq_dtype(logits.dtype), t, _ptr(ids), _ptr(weights),
-            _stream(stream)))
+            weights = _empty(shape, torch.float32, logits.device, stream)
+        if not (index >= 0 and _fits(logits, (t, self.num_experts), self._bf16 if bf16 else self._f32, index)
+                and _fits(ids, shape, self._i32, index) and _fits(weights, shape, self._f32, index)
+                and self._bias_index in (None, index)):
+            _need(logits, "logits", (t, self.num_experts), (torch.float32, torch.bfloat16))
+            _need(ids, "ids", shape, (torch.int32,))
+            _need(weights, "weights", shape, (torch.float32,))
+            _on_gpu(logits.device, logits=logits, bias=self.bias, ids=ids, weights=weights)
+        st = self._lib.moe_quant_gate_topk(self._ref, logits.data_ptr(), MQ_BF16 if bf16 else MQ_F32, t, ids.data_ptr(),
+                                           weights.data_ptr(), _raw_stream(stream, index))
+        if st:
+            _check(self._lib, st)
         return ids, weights
 
 
@@ -445,10 +462,13 @@ class ResidualNorm:
         _on_gpu(None, post_weight=post_weight, pre_weight=pre_weight)
         self.hidden, self.residual_dtype = hidden, residual_dtype
         self.post_weight, self.pre_weight = post_weight, pre_weight
+        self._bf16, self._types = torch.bfloat16, types
+        self._index = {w.get_device() for w in (post_weight, pre_weight) if w is not None}
         self.desc = NormDesc(ABI_VERSION, hidden, _mq_dtype(residual_dtype), _mq_dtype(weight_dtype), eps,
                              weight_offset, scale, _ptr(post_weight), _ptr(pre_weight))
+        self._ref = ctypes.byref(self.desc)
         # the library's own checks of the fields; no tokens, so nothing is enqueued
-        _check(self._lib, self._lib.moe_quant_norm(ctypes.byref(self.desc), None, None, None, GATE_NONE, 0, 0,
+        _check(self._lib, self._lib.moe_quant_norm(self._ref, None, None, None, GATE_NONE, 0, 0,
                                                    None, None, None))
 
     def forward(self, x=None, residual=None, gate=None, residual_out=None, norm_out=None, stream=None):
@@ -460,38 +480,46 @@ class ResidualNorm:
         first = x if x is not None else residual
         if first is None or first.dim() != 2:
             raise ValueError("need x or residual [T, H]")
-        t, h, dev = first.shape[0], self.hidden, first.device
-        if x is not None:
-            _need(x, "x", (t, h), (torch.bfloat16,))
-        if residual is not None:
-            _need(residual, "residual", (t, h), (self.residual_dtype,))
-        kind = GATE_NONE
-        if gate is not None:
-            shape = tuple(gate.shape)
-            kind = (GATE_CHANNEL if shape == (h,) else GATE_FULL if shape == (t, h)
-                    else GATE_TOKEN if shape == (t, 1) else None)
-            if kind is None:
-                raise ValueError(f"gate has shape {shape}, expected ({h},), ({t}, 1) or ({t}, {h})")
-            _need(gate, "gate", shape, (torch.float32, torch.bfloat16))
-        if not _is_current(first):
-            with torch.cuda.device(dev):
+        t, h, index = first.shape[0], self.hidden, first.get_device()
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return self.forward(x, residual, gate, residual_out, norm_out, stream)
+        shape, rd = (t, h), self.residual_dtype
+        kind, gate_dtype, gate_ptr = GATE_NONE, MQ_F32, None
+        if gate is not None:
+            gs = gate.shape
+            kind = (GATE_CHANNEL if gs == (h,) else GATE_FULL if gs == shape else GATE_TOKEN if gs == (t, 1) else None)
+            if kind is None:
+                raise ValueError(f"gate has shape {tuple(gs)}, expected ({h},), ({t}, 1) or ({t}, {h})")
+            gate_dtype, gate_ptr = _mq_dtype(gate.dtype), gate.data_ptr()
         if residual_out is None:
-            residual_out = _empty((t, h), self.residual_dtype, dev, stream)
-        _need(residual_out, "residual_out", (t, h), (self.residual_dtype,))
+            residual_out = _empty(shape, rd, first.device, stream)
         if self.pre_weight is None:
             if norm_out is not None:
                 raise ValueError("norm_out needs a pre_weight")
-        else:
-            if norm_out is None:
-                norm_out = _empty((t, h), torch.bfloat16, dev, stream)
-            _need(norm_out, "norm_out", (t, h), (torch.bfloat16,))
-        _on_gpu(dev, x=x, residual=residual, gate=gate, residual_out=residual_out, norm_out=norm_out,
-                post_weight=self.post_weight, pre_weight=self.pre_weight)
-        _check(self._lib, self._lib.moe_quant_norm(
-            ctypes.byref(self.desc), _ptr(x), _ptr(residual), _ptr(gate), kind,
-            MQ_F32 if gate is None else _mq_dtype(gate.dtype), t, _ptr(residual_out), _ptr(norm_out),
-            _stream(stream)))
+        elif norm_out is None:
+            norm_out = _empty(shape, self._bf16, first.device, stream)
+        if not (index >= 0 and (x is None or _fits(x, shape, self._bf16, index))
+                and (residual is None or _fits(residual, shape, rd, index)) and _fits(residual_out, shape, rd, index)
+                and (norm_out is None or _fits(norm_out, shape, self._bf16, index)) and self._index <= {index}
+                and (gate is None or gate.dtype in self._types and _fits(gate, gs, gate.dtype, index))):
+            if x is not None:
+                _need(x, "x", shape, (torch.bfloat16,))
+            if residual is not None:
+                _need(residual, "residual", shape, (rd,))
+            if gate is not None:
+                _need(gate, "gate", tuple(gs), self._types)
+            _need(residual_out, "residual_out", shape, (rd,))
+            if norm_out is not None:
+                _need(norm_out, "norm_out", shape, (torch.bfloat16,))
+            _on_gpu(first.device, x=x, residual=residual, gate=gate, residual_out=residual_out, norm_out=norm_out,
+                    post_weight=self.post_weight, pre_weight=self.pre_weight)
+        st = self._lib.moe_quant_norm(
+            self._ref, None if x is None else x.data_ptr(), None if residual is None else residual.data_ptr(), gate_ptr,
+            kind, gate_dtype, t, residual_out.data_ptr(), None if norm_out is None else norm_out.data_ptr(),
+            _raw_stream(stream, index))
+        if st:
+            _check(self._lib, st)
         return residual_out, norm_out
 
 
@@ -556,6 +584,14 @@ class Layer:
         _check(self._lib, self._lib.moe_quant_workspace_size(self._h, num_tokens, ctypes.byref(n)))
         return n.value
 
+    _last_need = (-1, 0)      # (tokens, bytes) of the last gated forward
+
+    def _workspace_need(self, num_tokens: int) -> int:
+        last = self._last_need
+        if last[0] != num_tokens:
+            last = self._last_need = (num_tokens, self.workspace_size(num_tokens))
+        return last[1]
+
     def workspace(self, num_tokens: int, device=None):
         import torch
         return torch.empty(max(self.workspace_size(num_tokens), 256), dtype=torch.uint8,
@@ -610,18 +646,35 @@ class Layer:
             raise ValueError("logits_out needs router_w")
         if hidden.dim() != 2:
             raise ValueError("hidden must be [T, H]")
-        if not _is_current(hidden):
-            with torch.cuda.device(hidden.device):
+        index, t, bf16 = hidden.get_device(), hidden.shape[0], torch.bfloat16
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return self.forward_gated(gate, hidden, logits, router_w, residual, out, workspace, activations,
                                           act_gscale13, act_gscale2, logits_out, probe, events, stream)
-        if gate.bias is not None:
+        if gate.bias is not None and gate.bias.device != self.device:
             _on_gpu(self.device, **{"gate.bias": gate.bias})
-        if stream is not None:
-            t = hidden.shape[0]
-            if out is None:
-                out = _empty((t, self.hidden), torch.bfloat16, self.device, stream)
-            if workspace is None:
-                workspace = _empty((max(self.workspace_size(t), 256),), torch.uint8, self.device, stream)
+        if out is None:
+            out = _empty((t, self.hidden), bf16, self.device, stream)
+        if workspace is None:
+            workspace = _empty((max(self.workspace_size(t), 256),), torch.uint8, self.device, stream)
+        shape, wide = (t, self.hidden), logits_out if logits is None else logits
+        if (probe is None and events is None and index == self.device.index and t > 0
+                and _fits(hidden, shape, bf16, index) and _fits(out, shape, bf16, index)
+                and (residual is None or _fits(residual, shape, bf16, index))
+                and (router_w is None or _fits(router_w, (self.num_experts, self.hidden), bf16, index))
+                and (wide is None or _fits(wide, (t, self.num_experts), torch.float32, index)
+                     or (logits is not None and _fits(logits, (t, self.num_experts), bf16, index)))
+                and workspace.is_contiguous() and workspace.get_device() == index
+                and _nbytes(workspace) >= self._workspace_need(t)):
+            # everything is as _forward's checks want it
+            st = self._lib.moe_quant_forward_gated(
+                self._h, gate._ref, _ptr(logits), MQ_BF16 if logits is not None and logits.dtype is bf16 else MQ_F32,
+                _ptr(router_w), hidden.data_ptr(), _ptr(residual), t, out.data_ptr(), workspace.data_ptr(),
+                _nbytes(workspace), ACTIVATIONS[activations], act_gscale13, act_gscale2, _ptr(logits_out), None,
+                _raw_stream(stream, index))
+            if st:
+                _check(self._lib, st)
+            return out
         return self._forward(logits, router_w, hidden, residual, out, workspace, probe, events, stream, logits_out,
                              gate=gate, act=(ACTIVATIONS[activations], float(act_gscale13), float(act_gscale2)))
 
@@ -677,7 +730,7 @@ class Layer:
         prp = ctypes.byref(pr) if pr is not None else None
         if gate is not None:
             st = self._lib.moe_quant_forward_gated(
-                self._h, ctypes.byref(gate.desc), _ptr(logits), MQ_F32 if logits is None else _mq_dtype(logits.dtype),
+                self._h, gate._ref, _ptr(logits), MQ_F32 if logits is None else _mq_dtype(logits.dtype),
                 _ptr(router_w), _ptr(hidden), _ptr(residual), t, _ptr(out), _ptr(workspace), _nbytes(workspace),
                 *act, _ptr(logits_out), prp, _stream(stream))
         elif router_w is None:

@@ -1,19 +1,26 @@
 // Gated routing: softmax or sigmoid scores, a balance bias that takes part in
 // the selection only, groups of experts of which a few are kept, top-k,
-// renormalised or raw weights (mq_gate in the C header states the formulas).
+// renormalised or raw weights (mq_gate in the C header states the formulas),
+// and the routing stage of an expert-layer forward under such a gate.
 //
 // The order of two selection scores next to each other decides which expert a
-// token takes, so the selection runs on 64-bit scores: sigmoid(l) + bias
-// rounds at 2^-54 there, against gaps of 2^-24 and less that a 32-bit score
-// cannot tell apart.
+// token takes.  A 32-bit score cannot tell apart what differs by less than its
+// rounding, so the selection is defined on 64-bit scores; the fast kernel
+// selects on 32-bit ones, bounds their error and hands the few tokens whose
+// order lies within it (and rows with too many equal scores) to the 64-bit one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "device.h"
 #include "internal.h"
 #include "route.h"
 
 namespace mq {
+
+constexpr float kInf = __builtin_inff();
+constexpr float kLog2e = 1.44269504088896340736f;
 
 // Order-preserving map of a double to an unsigned integer; -0 maps to the key
 // of +0, and no key of a number is 0 (the key of a selected or excluded expert).
@@ -23,11 +30,10 @@ __device__ __forceinline__ uint64_t ordered_key64(double v) {
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
-// A logit as the gate reads it: NaN counts as -inf (masked), +inf as the
-// largest finite value.
+// A logit or a bias as the gate reads it: NaN counts as -inf (masked), +inf as
+// the largest finite value, -0 as +0.
 __device__ __forceinline__ float gate_logit(float v) {
-  v = v == v ? v : -INFINITY;
-  return fminf(v, 3.402823466e38f);
+  return v == v ? fminf(v + 0.f, 3.402823466e38f) : -kInf;
 }
 __device__ __forceinline__ float load_gate_logit(const void *logits, int bf16, int64_t i) {
   return gate_logit(bf16 ? bf16_to_f32(((const uint16_t *)logits)[i]) : ((const float *)logits)[i]);
@@ -44,90 +50,88 @@ __device__ __forceinline__ float max64f(float v) {
   return fmaxf(v, __shfl_xor(v, 32, 64));
 }
 
-// Weight of the slot a lane holds (wave-wide; l = -inf where the expert is
-// masked or the lane has no slot).  m and z: softmax maximum and sum over all
-// experts.  Written so that nothing overflows and small scores keep their
-// digits: sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)), and a renormalised row
-// is shifted by its largest logit first.
-__device__ __forceinline__ float gate_weight(const GateArgs &g, float l, float m, float z) {
-  const float top = g.renormalize ? max64f(l) : 0.f;  // -inf where every slot is masked
-  float s = 0.f;
-  if (l > -INFINITY) {
-    if (g.score == MQ_SCORE_SIGMOID)
-      s = expf(fminf(l, 0.f) - (g.renormalize ? fminf(top, 0.f) : 0.f)) / (1.f + expf(-fabsf(l)));
-    else
-      s = g.renormalize ? expf(l - top) : expf(l - m) / z;
-  }
-  if (g.renormalize) {
-    const float sum = sum64f(s);
-    s = sum > 0.f ? s / sum : 0.f;
-  }
-  return s * g.scale;
+// The weight of a selected expert before its row is renormalised (0 where it is
+// masked, l = -inf).  top: the row's largest selected logit (used where it is
+// renormalised); m and z: softmax maximum and sum over all experts.  Written so
+// that nothing overflows and small scores keep their digits: sigmoid(l) =
+// exp(min(l, 0)) / (1 + exp(-|l|)), a renormalised row shifted by its largest.
+__device__ __forceinline__ float slot_score(const GateArgs &g, float l, float top, float m, float z) {
+  if (!(l > -kInf)) return 0.f;
+  if (g.score == MQ_SCORE_SIGMOID)
+    return expf(fminf(l, 0.f) - (g.renormalize ? fminf(top, 0.f) : 0.f)) / (1.f + expf(-fabsf(l)));
+  return g.renormalize ? expf(l - top) : expf(l - m) / z;
 }
 
-// The power of two that brings a token's largest weight into [2^-1, 1).
-__device__ __forceinline__ float weight_scale(float m) {
-  if (!(m > 0.f)) return 1.f;
+// The exponent of the power of two that brings a token's largest weight m into
+// [2^-1, 1).
+__device__ __forceinline__ int weight_exponent(float m) {
+  if (!(m > 0.f)) return 0;
   const int ex = (int)(__builtin_bit_cast(uint32_t, m) >> 23) - 126;
-  return pow2f(ex < -120 ? -120 : ex > 120 ? 120 : ex);
+  return ex < -120 ? -120 : ex > 120 ? 120 : ex;
 }
 
-// Orders a wave's LDS writes before its reads of other lanes' values.
+// down: the power of two taken out of the weights (1 where none is).
+__device__ __forceinline__ void write_slot(const GateOut &o, int64_t at, int id, float w, float down) {
+  o.ids[at] = id;
+  o.wts[at] = w * down;
+  if (o.p_ids) o.p_ids[at] = id;
+  if (o.p_w) o.p_w[at] = w;
+}
+
+// Orders a wave's LDS writes before its reads of other lanes' values (and the
+// other way round); each wave uses LDS of its own, so no barrier is needed.
 __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// ---------------------------------------------------------------------------
 // The gate of one token on all 64 lanes of a wave, in 64 bits; any number of
-// groups.  Lane l holds experts l + 64 i.  sc: one double per expert, LDS of
-// this wave alone.
-template <int kPer>
+// groups, any k.  Lane l holds experts l + 64 i; their scores, then their keys
+// (0: selected or excluded) lie in sc, E doubles of LDS of this wave alone, so
+// that the fast kernel's registers are not held for this path.  Each of the k
+// rounds takes the largest key (two 32-bit maxima) and the lowest expert that
+// holds it.
+// ---------------------------------------------------------------------------
 __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__restrict__ logits, int bf16, int64_t t,
                                            int lane, double *sc, const GateOut &o) {
-  float l[kPer];
-  uint64_t key[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < g.E ? load_gate_logit(logits, bf16, t * g.E + e) : -INFINITY;
-  }
+  const int64_t at = t * g.E;
   // softmax statistics over the live logits (M = 0 where there is none)
-  float m = l[0];
-#pragma unroll
-  for (int i = 1; i < kPer; ++i) m = fmaxf(m, l[i]);
+  float m = -kInf;
+#pragma unroll 1
+  for (int e = lane; e < g.E; e += 64) m = fmaxf(m, load_gate_logit(logits, bf16, at + e));
   m = max64f(m);
-  if (m == -INFINITY) m = 0.f;
+  if (m == -kInf) m = 0.f;
   double z = 0.0;
   if (g.score == MQ_SCORE_SOFTMAX) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) z += exp((double)l[i] - (double)m);
+#pragma unroll 1
+    for (int e = lane; e < g.E; e += 64) z += exp((double)load_gate_logit(logits, bf16, at + e) - (double)m);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) z += __shfl_xor(z, d, 64);
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = 0ull;
-    if (e < g.E) {
-      const float b = g.bias ? g.bias[e] : 0.f;
-      const bool live = l[i] > -INFINITY && b > -INFINITY;
-      double c = -INFINITY;
-      // without a bias the order is the logits' own; the score itself is
-      // needed for sums of two only
-      if (live)
-        c = !g.bias && g.group_top == 1 ? (double)l[i]
-            : g.score == MQ_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)l[i])) + (double)b
-                                          : exp((double)l[i] - (double)m) / z + (double)b;
-      sc[e] = c;
-      if (live && !g.bias) c = (double)l[i];
-      key[i] = ordered_key64(c);
+  const bool by_logit = g.bias == nullptr;  // the logits' order is the scores'
+  wave_lds_fence();
+#pragma unroll 1
+  for (int e = lane; e < g.E; e += 64) {
+    const float l = load_gate_logit(logits, bf16, at + e), b = g.bias ? gate_logit(g.bias[e]) : 0.f;
+    double c = -kInf;
+    if (l > -kInf && b > -kInf) {
+      // the score itself is needed for sums of two and beside a bias only
+      const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
+      c = l;
+      if (!by_logit || g.group_top == 2) {
+        const double p = exp(sigmoid ? -(double)l : (double)l - (double)m);
+        c = (sigmoid ? 1.0 / (1.0 + p) : p / z) + (double)b;
+      }
     }
+    sc[e] = c;
   }
+  uint64_t kept = ~0ull;  // groups
   if (g.groups > 1) {
     // lane = group: its score, then the number of groups that come before it
     wave_lds_fence();
-    double s1 = -INFINITY, s2 = -INFINITY;
+    double s1 = -kInf, s2 = -kInf;
     if (lane < g.groups)
       for (int i = 0; i < g.per; ++i) {
         const double v = sc[lane * g.per + i];
@@ -138,73 +142,413 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
     const uint64_t gk = lane < g.groups ? ordered_key64(s) : 0ull;
     int before = 0;
     for (int j = 0; j < g.groups; ++j) {
-      const uint64_t o = __shfl(gk, j, 64);
-      before += o > gk || (o == gk && j < lane);
+      const uint64_t other = __shfl(gk, j, 64);
+      before += other > gk || (other == gk && j < lane);
     }
-    const uint64_t kept = __ballot(lane < g.groups && before < g.topk_groups);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 64 * i;
-      if (e < g.E && !((kept >> (e / g.per)) & 1ull)) key[i] = 0ull;
-    }
+    kept = __ballot(lane < g.groups && before < g.topk_groups);
+    wave_lds_fence();
+  }
+  uint64_t *key = (uint64_t *)sc;  // each lane its own experts' from here on
+#pragma unroll 1
+  for (int e = lane; e < g.E; e += 64) {
+    double c = sc[e];
+    if (by_logit && g.group_top == 2) c = load_gate_logit(logits, bf16, at + e);
+    key[e] = (kept >> (e / g.per)) & 1ull ? ordered_key64(c) : 0ull;
   }
   int slot_id = 0;
   for (int j = 0; j < g.k; ++j) {
-    uint64_t km = key[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) km = key[i] > km ? key[i] : km;
-    km = max64_u64(km);
-    uint32_t lo = 0u;  // ~id of the lowest expert that holds the maximum
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) lo = max(lo, key[i] == km ? 0xFFFFFFFFu - (uint32_t)(lane + 64 * i) : 0u);
-    const int e = (int)(0xFFFFFFFFu - max64_u32(lo));
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 64 * i == e) key[i] = 0ull;
+    uint64_t mine = 0ull;  // the lane's largest key, and the lowest expert that holds it
+    int e_mine = 0;
+#pragma unroll 1
+    for (int e = lane; e < g.E; e += 64) {
+      const uint64_t v = key[e];
+      if (v > mine) {
+        mine = v;
+        e_mine = e;
+      }
+    }
+    const uint64_t km = max64_u64(mine);
+    const int e = (int)(0xFFFFFFFFu - max64_u32(mine == km ? 0xFFFFFFFFu - (uint32_t)e_mine : 0u));
+    if (mine == km && e_mine == e) key[e] = 0ull;
     if (j == lane) slot_id = e;
   }
   // weights of the k slots (lane = slot), in 32 bits
-  float lw = -INFINITY;
+  float lw = -kInf;
   if (lane < g.k) {
-    lw = load_gate_logit(logits, bf16, t * g.E + slot_id);
-    const float b = g.bias ? g.bias[slot_id] : 0.f;
-    if (!(b > -INFINITY)) lw = -INFINITY;
+    lw = load_gate_logit(logits, bf16, at + slot_id);
+    if (g.bias && gate_logit(g.bias[slot_id]) == -kInf) lw = -kInf;
   }
-  const float w = gate_weight(g, lw, m, (float)z);
-  float ws = 1.f;
+  float w = slot_score(g, lw, g.renormalize ? max64f(lw) : 0.f, m, (float)z);
+  if (g.renormalize) {
+    const float sum = sum64f(w);
+    w = sum > 0.f ? w / sum : 0.f;
+  }
+  w *= g.scale;
+  float down = 1.f;
   if (o.wscale) {
-    ws = weight_scale(max64f(fabsf(w)));
-    if (lane == 0) o.wscale[t] = ws;
+    const int ex = weight_exponent(max64f(fabsf(w)));
+    down = pow2f(-ex);
+    if (lane == 0) o.wscale[t] = pow2f(ex);
   }
-  if (lane < g.k) {
-    const int64_t at = t * g.k + lane;
-    o.ids[at] = slot_id;
-    o.wts[at] = w / ws;  // exact: ws is a power of two
-    if (o.p_ids) o.p_ids[at] = slot_id;
-    if (o.p_w) o.p_w[at] = w;
-  }
+  if (lane < g.k) write_slot(o, t * g.k + lane, slot_id, w, down);
 }
 
-template <int kPer>
+// ---------------------------------------------------------------------------
+// The gate of four tokens on one wave, 16 lanes (one DPP row) per token, in 32
+// bits; groups 1, 2, 4, 8 or 16 and k <= 16.  A lane's kPer experts are
+// consecutive and of one group, so group scores are reductions over adjacent
+// lanes and equal scores lie in expert order over the lanes.
+//   1. scores as ordered integer keys, the two largest of each lane, and from
+//      those the group scores and the rank of each group;
+//   2. a lower bound tau of the k-th largest key: k rounds of "largest of the
+//      lanes' two largest", 4 DPP steps each;
+//   3. the experts at or above tau (8.2 of 256 on average for k = 8) go to LDS
+//      in expert order;
+//   4. each lane ranks the candidate it holds by counting those before it.
+// What is not certain at 32 bits: a score is off by at most 2^-22 + 2^-24 |c|
+// for a sigmoid (exponent 2^-23 |l| s(1 - s) <= 2^-25, reciprocal and sums) and
+// 2^-19 + 2^-24 |c| for a softmax (its sum over 512 experts, 32 a lane), so two
+// scores further apart than tol = 2^-19 (1 + |c|), for a softmax 2^-17 (1 +
+// |c|), are in their order.  tau is lowered by tol; a token is unsure where two
+// candidates next to each other in the order are within tol and not the same
+// logit and bias, or a kept and a dropped group are within 2 tol.  Without a
+// bias the keys are the logits and exact.  Masked and excluded experts share
+// the key 0: a token that needs them, or has more than 16 candidates (equal
+// scores), is unsure too.  Returns the unsure tokens (rows of the wave) as a
+// mask; the others are written.
+// ---------------------------------------------------------------------------
+constexpr int kFastK = 16;  // slots, and candidates a token may have
+
+struct Candidates {  // of one token, in LDS
+  uint32_t key[kFastK];
+  float l[kFastK];
+  int32_t id[kFastK];
+};
+
+// The value N lanes down the 16-lane row, 0 where the row has none.
+template <int N>
+__device__ __forceinline__ uint32_t dpp_shr(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x110 + N, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t min16_u32(uint32_t v) {
+  v = min(v, dpp<kXor1>(v));
+  v = min(v, dpp<kXor2>(v));
+  v = min(v, dpp<kHalfMirror>(v));
+  v = min(v, dpp<kMirror>(v));
+  return v;
+}
+// Key of a score that is no NaN and no -0; from_ordered_key inverts it.
+__device__ __forceinline__ uint32_t score_key(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // of -inf
+
+// The two largest of a pair of lanes' two largest.
+template <int kCtrl>
+__device__ __forceinline__ void top2_join(uint32_t &a, uint32_t &b) {
+  const uint32_t c = dpp<kCtrl>(a), d = dpp<kCtrl>(b);
+  b = max(min(a, c), max(b, d));
+  a = max(a, c);
+}
+// Number of other groups in the 16-lane row whose key comes before this lane's,
+// groups being `lanes` lanes wide; equal keys count where the other group is
+// the lower one (bit n of lower: the lane n places down the row).
+template <int N>
+__device__ __forceinline__ int groups_before(uint32_t key, uint32_t lower, int lanes) {
+  int before = 0;
+  if constexpr (N < 16) {
+    if ((N & (lanes - 1)) == 0) {  // uniform
+      const uint32_t other = dpp<0x120 + N>(key);  // row_ror
+      before = other > key - ((lower >> N) & 1u);
+    }
+    before += groups_before<N + 1>(key, lower, lanes);
+  }
+  return before;
+}
+
+// A lane's place in the gate.
+struct GateLane {
+  int lanes;       // lanes of a group
+  int e0, count;   // first expert of this lane, and how many
+  uint32_t lower;  // bit n: the lane n places down the row is of a lower group
+};
+template <int kPer, bool kFull>
+__device__ __forceinline__ GateLane gate_lane(const GateArgs &g, int li) {
+  GateLane a;
+  const int shift = 4 - (31 - __builtin_clz(g.groups));
+  a.lanes = 1 << shift;
+  const int off = li & (a.lanes - 1);
+  const int chunk = kFull ? kPer : (g.per + a.lanes - 1) >> shift;
+  a.e0 = kFull ? li * kPer : (li >> shift) * g.per + off * chunk;
+  a.count = kFull ? kPer : max(0, min(chunk, g.per - off * chunk));
+  a.lower = ((2u << li) - 1u) & ~((2u << off) - 1u);
+  return a;
+}
+
+template <int kPer, bool kFull>
+__device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *__restrict__ logits, int bf16,
+                                                 int64_t t0, int64_t T, int lane, Candidates *cands,
+                                                 const GateOut &o) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  typedef f4 f4_a4 __attribute__((aligned(4)));
+  const int li = lane & 15, row = lane >> 4;
+  const bool here = t0 + row < T;
+  const int64_t t = here ? t0 + row : T - 1;  // a row past the last token repeats it
+  const GateLane a = gate_lane<kPer, kFull>(g, li);
+  const bool softmax = g.score == MQ_SCORE_SOFTMAX, by_logit = g.bias == nullptr, sums = g.group_top == 2;
+  const float tol1 = softmax ? 0x1p-17f : 0x1p-19f;
+  float l[kPer];
+  const int64_t at = t * g.E + a.e0;
+  if (bf16) {
+    const uint16_t *p = (const uint16_t *)logits + at;
+    if (kFull) {
+      u2 u[kPer / 4];
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) u[i] = *(const u2 *)(p + 4 * i);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t w = u[i / 4][(i >> 1) & 1];
+        l[i] = __builtin_bit_cast(float, i & 1 ? w & 0xFFFF0000u : w << 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) l[i] = i < a.count ? bf16_to_f32(p[i]) : -kInf;
+    }
+  } else {
+    const float *p = (const float *)logits + at;
+    if (kFull) {
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) {
+        const f4 u = *(const f4 *)(p + 4 * i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) l[4 * i + q] = u[q];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) l[i] = i < a.count ? p[i] : -kInf;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) l[i] = gate_logit(l[i]);
+
+  // softmax statistics, where a score or a weight needs them
+  float m = 0.f, z = 1.f;
+  if (softmax && (!by_logit || !g.renormalize || sums)) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, l[i]);
+    m = max16f(m);
+    if (m == -kInf) m = 0.f;
+    if (!by_logit || !g.renormalize) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) z += __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
+      z = sum16(z);
+    }
+  }
+  // selection keys; 0: masked
+  uint32_t key[kPer];
+  if (by_logit) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = score_key(l[i]);
+  } else {
+    float c[kPer];
+    if (kFull) {
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) {
+        const f4 u = *(const f4_a4 *)(g.bias + a.e0 + 4 * i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[4 * i + q] = u[q];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = i < a.count ? g.bias[a.e0 + i] : -kInf;
+    }
+    if (softmax) {
+      const float zinv = 1.f / z;  // inf where every expert is masked: not used then
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        c[i] = gate_logit(c[i]) + __builtin_amdgcn_exp2f((l[i] - m) * kLog2e) * zinv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        c[i] = gate_logit(c[i]) + __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = l[i] == -kInf ? 0u : score_key(c[i]);
+  }
+  uint32_t t1 = 0u, t2 = 0u;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    key[i] = key[i] <= kMaskedKey ? 0u : key[i];
+    t2 = max(t2, min(t1, key[i]));
+    t1 = max(t1, key[i]);
+  }
+  bool unsure = false, kept = true;
+  if (g.groups > 1) {
+    uint32_t k1 = t1, k2 = t2;
+    if (a.lanes >= 2) top2_join<kXor1>(k1, k2);
+    if (a.lanes >= 4) top2_join<kXor2>(k1, k2);
+    if (a.lanes >= 8) top2_join<kHalfMirror>(k1, k2);
+    uint32_t gk = k1;
+    float size = 0.f;
+    if (sums || !by_logit) {
+      float s1 = from_ordered_key(max(k1, kMaskedKey)), s2 = from_ordered_key(max(k2, kMaskedKey));
+      if (by_logit) {  // the scores of the two logits (a softmax's without its common factor 1 / z)
+        s1 = s1 == -kInf ? s1 : softmax ? expf(s1 - m) : 1.f / (1.f + expf(-s1));
+        s2 = s2 == -kInf ? s2 : softmax ? expf(s2 - m) : 1.f / (1.f + expf(-s2));
+      }
+      size = fmaxf(fabsf(s1), sums ? fabsf(s2) : 0.f);
+      size = size < kInf ? size : 0.f;
+      gk = score_key((sums ? s1 + s2 : s1) + 0.f);
+    }
+    kept = groups_before<1>(gk, a.lower, a.lanes) < g.topk_groups;
+    if (sums || !by_logit) {
+      const float lo = from_ordered_key(min16_u32(kept ? gk : 0xFFFFFFFFu));
+      const float hi = from_ordered_key(max16_u32(kept ? 0u : gk));
+      // -inf on either side is exact (masked experts): the difference is then inf or NaN
+      unsure = g.topk_groups < g.groups && lo - hi <= 2.f * tol1 * (1.f + max16f(size));
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = kept ? key[i] : 0u;
+  }
+  t1 = kept ? t1 : 0u;
+  t2 = kept ? t2 : 0u;
+  uint32_t tau = 0u;
+  for (int j = 0; j < g.k; ++j) {
+    tau = max16_u32(t1);
+    const bool out = t1 == tau;  // several lanes may go at once: tau only gets lower
+    t1 = out ? t2 : t1;
+    t2 = out ? 0u : t2;
+  }
+  if (!by_logit && tau != 0u) {
+    const float v = from_ordered_key(tau);
+    tau = max(score_key((v - tol1 * (1.f + fabsf(v))) + 0.f), 1u);
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) n += key[i] >= tau;
+  int pos = n;  // inclusive sum over the row's lanes
+  pos += (int)dpp_shr<1>(pos);
+  pos += (int)dpp_shr<2>(pos);
+  pos += (int)dpp_shr<4>(pos);
+  pos += (int)dpp_shr<8>(pos);
+  const int have = __shfl(pos, 15, 16);
+  pos -= n;
+  // tau 0: fewer than k live experts among the lanes' two largest
+  const bool fits = tau != 0u && have <= kFastK;
+  unsure |= !fits;
+  tau = fits ? tau : 0xFFFFFFFFu;  // no key is that large
+  Candidates &cd = cands[row];
+  wave_lds_fence();
+  cd.key[li] = 0u;
+  wave_lds_fence();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (key[i] >= tau) {
+      cd.key[pos] = key[i];
+      cd.l[pos] = l[i];
+      cd.id[pos] = a.e0 + i;
+      ++pos;
+    }
+  wave_lds_fence();
+  const uint32_t ck = cd.key[li];  // 0: no candidate
+  const float cl = cd.l[li];
+  const int id = cd.id[li];
+  int rank = 0;
+#pragma unroll
+  for (int p = 0; p < kFastK; ++p) rank += cd.key[p] > ck - (p < li ? 1u : 0u);  // equal keys: in expert order
+  if (!by_logit) {
+    // neighbours in the order, through LDS
+    wave_lds_fence();
+    if (ck != 0u) {
+      cd.key[rank] = ck;
+      cd.l[rank] = cl;
+      cd.id[rank] = id;
+    }
+    wave_lds_fence();
+    const int next = min(rank + 1, kFastK - 1);
+    const float c = from_ordered_key(ck), d = from_ordered_key(cd.key[next]);
+    if (fits && rank + 1 < have && c - d <= tol1 * (1.f + fabsf(c)))
+      unsure |= cl != cd.l[next] || gate_logit(g.bias[id]) != gate_logit(g.bias[cd.id[next]]);
+  }
+  const uint64_t votes = __ballot(unsure && here);
+  uint32_t redo = 0u;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) redo |= (uint32_t)(((votes >> (16 * r)) & 0xFFFFull) != 0ull) << r;
+
+  // weights of the selected candidates
+  const bool sel = fits && ck != 0u && rank < g.k;
+  const float top = g.renormalize ? max16f(sel ? cl : -kInf) : 0.f;
+  float w = slot_score(g, sel ? cl : -kInf, top, m, z);
+  if (g.renormalize) {
+    const float sum = sum16(w);
+    w = sum > 0.f ? w / sum : 0.f;
+  }
+  w *= g.scale;
+  const bool done = here && !((redo >> row) & 1u);
+  float down = 1.f;
+  if (o.wscale) {
+    const int ex = weight_exponent(max16f(fabsf(w)));
+    down = pow2f(-ex);
+    if (done && li == 0) o.wscale[t] = pow2f(ex);
+  }
+  if (done && sel) write_slot(o, t * g.k + rank, id, w, down);
+  return redo;
+}
+
+// Four tokens (from t0 on) of one wave: the fast gate, then the 64-bit one for
+// the tokens it could not decide.  kPer 0: the 64-bit one alone, for k above 16
+// or a number of groups that does not divide a row of lanes.
+union GateLds {
+  Candidates cand[4];
+  double sc[kMaxExperts];
+};
+template <int kPer, bool kFull>
+__device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restrict__ logits, int bf16, int64_t t0,
+                                          int64_t T, int lane, GateLds *lds, const GateOut &o) {
+  uint32_t redo = 0xFu;
+  if constexpr (kPer > 0) redo = gate_tokens4<kPer, kFull>(g, logits, bf16, t0, T, lane, lds->cand, o);
+  for (int r = 0; r < 4 && t0 + r < T; ++r)
+    if ((redo >> r) & 1u) gate_token(g, logits, bf16, t0 + r, lane, lds->sc, o);
+}
+
+template <int kPer, bool kFull>
 __global__ __launch_bounds__(256) void gate_topk_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                         int64_t T, GateOut o) {
-  __shared__ double sc[4][64 * kPer];
+  __shared__ GateLds lds[4];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  if (t >= T) return;  // no barrier below: each wave has its own scores
-  gate_token<kPer>(g, logits, bf16, t, lane, sc[wave], o);
+  const int64_t t0 = ((int64_t)blockIdx.x * (blockDim.x >> 6) + wave) * 4;
+  if (t0 < T) gate_wave<kPer, kFull>(g, logits, bf16, t0, T, lane, &lds[wave], o);
+}
+
+// Calls f with the kernel variant for this gate: f(kPer, kFull) as constants.
+template <typename F>
+static hipError_t with_gate_variant(const GateArgs &g, F f) {
+  using std::integral_constant;
+  const int lanes = 16 / g.groups;  // 0 above 16 groups
+  if (g.k > kFastK || lanes == 0 || 16 % g.groups) return f(integral_constant<int, 0>{}, integral_constant<bool, false>{});
+  const int chunk = (g.per + lanes - 1) / lanes;
+  const bool full = chunk * 16 == g.E;
+  auto go = [&](auto n) {
+    return full && chunk == n() ? f(n, integral_constant<bool, true>{}) : f(n, integral_constant<bool, false>{});
+  };
+  if (chunk <= 4) return go(integral_constant<int, 4>{});
+  if (chunk <= 8) return go(integral_constant<int, 8>{});
+  if (chunk <= 16) return go(integral_constant<int, 16>{});
+  return go(integral_constant<int, 32>{});
 }
 
 hipError_t launch_gate_topk(const GateArgs &g, const void *logits, int bf16, int64_t T, const GateOut &o,
                             hipStream_t s) {
-  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
-  if (g.E <= 128)
-    hipLaunchKernelGGL(gate_topk_kernel<2>, grid, block, 0, s, g, logits, bf16, T, o);
-  else if (g.E <= 256)
-    hipLaunchKernelGGL(gate_topk_kernel<4>, grid, block, 0, s, g, logits, bf16, T, o);
-  else
-    hipLaunchKernelGGL(gate_topk_kernel<8>, grid, block, 0, s, g, logits, bf16, T, o);
-  return hipGetLastError();
+  return with_gate_variant(g, [&](auto per, auto full) {
+    // one wave a workgroup spreads a small batch over the CUs
+    const int threads = T <= 4096 ? 64 : 256, tpb = threads / 16;
+    hipLaunchKernelGGL((gate_topk_kernel<per(), full()>), dim3((unsigned)((T + tpb - 1) / tpb)), dim3(threads), 0, s, g,
+                       logits, bf16, T, o);
+    return hipGetLastError();
+  });
 }
 
 // Hidden rows of 4 tokens per wave for a gated forward, staged as route_kernel
