@@ -88,56 +88,71 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 // ---------------------------------------------------------------------------
 // The gate of one token on all 64 lanes of a wave, in 64 bits; any number of
-// groups, any k.  Lane l holds experts l + 64 i; their scores, then their keys
-// (0: selected or excluded) lie in sc, E doubles of LDS of this wave alone, so
-// that the fast kernel's registers are not held for this path.  Each of the k
-// rounds takes the largest key (two 32-bit maxima) and the lowest expert that
-// holds it.
+// groups, any k.  Lane l holds experts l + 64 i.  sc: one double per expert, LDS
+// of this wave alone (the group scores read other lanes' experts there).  Each
+// of the k rounds takes the largest key (two 32-bit maxima) and the lowest
+// expert that holds it.  The exponentials stay one after the other (sched
+// barriers): interleaved they would take the registers of the fast kernel.
 // ---------------------------------------------------------------------------
+template <int kPer>
 __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__restrict__ logits, int bf16, int64_t t,
                                            int lane, double *sc, const GateOut &o) {
   const int64_t at = t * g.E;
+  float l[kPer], b[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 64 * i;
+    l[i] = e < g.E ? load_gate_logit(logits, bf16, at + e) : -kInf;
+    b[i] = g.bias && e < g.E ? gate_logit(g.bias[e]) : 0.f;
+  }
   // softmax statistics over the live logits (M = 0 where there is none)
-  float m = -kInf;
-#pragma unroll 1
-  for (int e = lane; e < g.E; e += 64) m = fmaxf(m, load_gate_logit(logits, bf16, at + e));
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < kPer; ++i) m = fmaxf(m, l[i]);
   m = max64f(m);
   if (m == -kInf) m = 0.f;
-  double z = 0.0;
-  if (g.score == MQ_SCORE_SOFTMAX) {
-#pragma unroll 1
-    for (int e = lane; e < g.E; e += 64) z += exp((double)load_gate_logit(logits, bf16, at + e) - (double)m);
+  const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
+  const bool by_logit = g.bias == nullptr;              // the logits' order is the scores'
+  const bool scores = !by_logit || g.group_top == 2;    // else the order alone is enough
+  double c[kPer], z = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    c[i] = l[i];
+    if (scores || (!sigmoid && !g.renormalize)) {
+      c[i] = exp(sigmoid ? -(double)l[i] : (double)l[i] - (double)m);
+      z += c[i];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (!sigmoid) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) z += __shfl_xor(z, d, 64);
   }
-  const bool by_logit = g.bias == nullptr;  // the logits' order is the scores'
+  uint64_t key[kPer];
   wave_lds_fence();
-#pragma unroll 1
-  for (int e = lane; e < g.E; e += 64) {
-    const float l = load_gate_logit(logits, bf16, at + e), b = g.bias ? gate_logit(g.bias[e]) : 0.f;
-    double c = -kInf;
-    if (l > -kInf && b > -kInf) {
-      // the score itself is needed for sums of two and beside a bias only
-      const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
-      c = l;
-      if (!by_logit || g.group_top == 2) {
-        const double p = exp(sigmoid ? -(double)l : (double)l - (double)m);
-        c = (sigmoid ? 1.0 / (1.0 + p) : p / z) + (double)b;
-      }
-    }
-    sc[e] = c;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 64 * i;
+    const bool live = l[i] > -kInf && b[i] > -kInf;
+    double s = l[i];
+    if (scores) s = (sigmoid ? 1.0 / (1.0 + c[i]) : c[i] / z) + (double)b[i];
+    if (!live) s = -kInf;
+    if (g.groups > 1 && e < g.E) sc[e] = s;
+    key[i] = e < g.E ? ordered_key64(by_logit ? (double)l[i] : s) : 0ull;
+    __builtin_amdgcn_sched_barrier(0);
   }
-  uint64_t kept = ~0ull;  // groups
   if (g.groups > 1) {
     // lane = group: its score, then the number of groups that come before it
     wave_lds_fence();
     double s1 = -kInf, s2 = -kInf;
-    if (lane < g.groups)
+    if (lane < g.groups) {
+#pragma unroll 4
       for (int i = 0; i < g.per; ++i) {
         const double v = sc[lane * g.per + i];
         s2 = fmax(s2, fmin(s1, v));
         s1 = fmax(s1, v);
       }
+    }
     const double s = g.group_top == 2 ? s1 + s2 : s1;
     const uint64_t gk = lane < g.groups ? ordered_key64(s) : 0ull;
     int before = 0;
@@ -145,31 +160,26 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
       const uint64_t other = __shfl(gk, j, 64);
       before += other > gk || (other == gk && j < lane);
     }
-    kept = __ballot(lane < g.groups && before < g.topk_groups);
-    wave_lds_fence();
-  }
-  uint64_t *key = (uint64_t *)sc;  // each lane its own experts' from here on
-#pragma unroll 1
-  for (int e = lane; e < g.E; e += 64) {
-    double c = sc[e];
-    if (by_logit && g.group_top == 2) c = load_gate_logit(logits, bf16, at + e);
-    key[e] = (kept >> (e / g.per)) & 1ull ? ordered_key64(c) : 0ull;
+    const uint64_t kept = __ballot(lane < g.groups && before < g.topk_groups);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (!((kept >> (min(lane + 64 * i, g.E - 1) / g.per)) & 1ull)) key[i] = 0ull;
   }
   int slot_id = 0;
   for (int j = 0; j < g.k; ++j) {
-    uint64_t mine = 0ull;  // the lane's largest key, and the lowest expert that holds it
-    int e_mine = 0;
-#pragma unroll 1
-    for (int e = lane; e < g.E; e += 64) {
-      const uint64_t v = key[e];
-      if (v > mine) {
-        mine = v;
-        e_mine = e;
+    uint64_t mine = key[0];  // the lane's largest key, and the lowest expert that holds it
+    int e_mine = lane;
+#pragma unroll
+    for (int i = 1; i < kPer; ++i)
+      if (key[i] > mine) {
+        mine = key[i];
+        e_mine = lane + 64 * i;
       }
-    }
     const uint64_t km = max64_u64(mine);
     const int e = (int)(0xFFFFFFFFu - max64_u32(mine == km ? 0xFFFFFFFFu - (uint32_t)e_mine : 0u));
-    if (mine == km && e_mine == e) key[e] = 0ull;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 64 * i == e) key[i] = 0ull;
     if (j == lane) slot_id = e;
   }
   // weights of the k slots (lane = slot), in 32 bits
@@ -510,8 +520,9 @@ __device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restr
                                           int64_t T, int lane, GateLds *lds, const GateOut &o) {
   uint32_t redo = 0xFu;
   if constexpr (kPer > 0) redo = gate_tokens4<kPer, kFull>(g, logits, bf16, t0, T, lane, lds->cand, o);
+  constexpr int kPer64 = kPer == 0 ? kMaxExperts / 64 : kPer <= 4 ? 1 : kPer / 4;
   for (int r = 0; r < 4 && t0 + r < T; ++r)
-    if ((redo >> r) & 1u) gate_token(g, logits, bf16, t0 + r, lane, lds->sc, o);
+    if ((redo >> r) & 1u) gate_token<kPer64>(g, logits, bf16, t0 + r, lane, lds->sc, o);
 }
 
 template <int kPer, bool kFull>
