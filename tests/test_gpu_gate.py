@@ -174,6 +174,40 @@ def test_far_logits(kind):
         check(lg, 8, **KINDS[kind])
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid_raw"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("e,k,groups,topk_groups", [(512, 12, 1, 1), (256, 8, 8, 1), (512, 8, 16, 4), (128, 8, 4, 1),
+                                                    (256, 16, 8, 2), (160, 16, 1, 1)])
+def test_scores_bunched_in_few_lanes(kind, with_bias, e, k, groups, topk_groups):
+    """The best experts next to each other, in falling and rising order: many
+    candidates in a lane, and groups that keep few lanes."""
+    lg = logits(40, e, seed=k)
+    lg[:10] = torch.linspace(3, -3, e, device="cuda")
+    lg[10:20] = torch.linspace(-3, 3, e, device="cuda")
+    lg[20:30, e // 2:e // 2 + 40] += 4
+    check(lg, k, bias=a_bias(e, size=0.01) if with_bias else None, groups=groups, topk_groups=topk_groups,
+          group_top=2 if groups > 1 else 1, **KINDS[kind])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_closer_than_a_32_bit_rounding(score):
+    """Group sums that differ by 2^-26 and less, equal ones, and groups whose
+    three best experts lie within 2^-24."""
+    t, e, groups = 64, 128, 8
+    gen = np.random.default_rng(7)
+    lg = np.zeros((t, e), np.float32)
+    top = gen.normal(size=(t, 1, 3)).astype(np.float32) + 3
+    lg.reshape(t, groups, 16)[:] = gen.normal(size=(t, groups, 16)) - 2
+    lg.reshape(t, groups, 16)[:, :, 4:7] = top
+    lg.reshape(t, groups, 16)[20:40, :, 9] = top[20:40, :, 0]
+    bias = (gen.integers(-4, 4, e) * 2.0 ** -27).astype(np.float32)
+    wide = (gen.integers(-4, 4, e) * 2.0 ** -23).astype(np.float32)
+    for b in (bias, wide, None):
+        for top_n in (1, 2):
+            check(torch.from_numpy(lg).cuda(), 6, bias=None if b is None else torch.from_numpy(b).cuda(), score=score,
+                  groups=groups, topk_groups=3, group_top=top_n)
+
+
 def test_many_tokens_and_limits():
     check(logits(5000, 64, seed=9), 4, bias=a_bias(64), score="sigmoid", groups=8, topk_groups=4, group_top=2, scale=2.5)
     g = Gate(16, 2)

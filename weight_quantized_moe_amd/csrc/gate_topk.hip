@@ -219,17 +219,21 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
 // for a sigmoid (exponent 2^-23 |l| s(1 - s) <= 2^-25, reciprocal and sums) and
 // 2^-19 + 2^-24 |c| for a softmax (its sum over 512 experts, 32 a lane), so two
 // scores further apart than tol = 2^-19 (1 + |c|), for a softmax 2^-17 (1 +
-// |c|), are in their order.  tau is lowered by tol; a token is unsure where two
-// candidates next to each other in the order are within tol and not the same
-// logit and bias, or a kept and a dropped group are within 2 tol.  Without a
-// bias the keys are the logits and exact.  Masked and excluded experts share
-// the key 0: a token that needs them, or has more than 16 candidates (equal
-// scores), is unsure too.  Returns the unsure tokens (rows of the wave) as a
-// mask; the others are written.
+// |c|), are in their order.  tau is lowered by tol.  Where two candidates next
+// to each other in the order are within tol and not the same logit and bias,
+// the row's candidates are ranked again by 64-bit scores; where a kept and a
+// dropped group are within 2 tol, the groups are, by the 64-bit scores of each
+// lane's two largest.  Without a bias the keys are the logits and exact, and
+// masked experts (key of -inf) are exact always: of more than 16 candidates
+// those equal to tau then count in expert order only.  What is left (more than
+// 16 candidates or three scores of a lane within tol) is handed to the 64-bit
+// gate: returns those tokens (rows of the wave) as a mask; the others are
+// written.
 // ---------------------------------------------------------------------------
 constexpr int kFastK = 16;  // slots, and candidates a token may have
 
 struct Candidates {  // of one token, in LDS
+  uint64_t wide[kFastK];
   uint32_t key[kFastK];
   float l[kFastK];
   int32_t id[kFastK];
@@ -247,12 +251,64 @@ __device__ __forceinline__ uint32_t min16_u32(uint32_t v) {
   v = min(v, dpp<kMirror>(v));
   return v;
 }
+__device__ __forceinline__ int sum16i(int v) {
+  v += (int)dpp<kXor1>((uint32_t)v);
+  v += (int)dpp<kXor2>((uint32_t)v);
+  v += (int)dpp<kHalfMirror>((uint32_t)v);
+  v += (int)dpp<kMirror>((uint32_t)v);
+  return v;
+}
+// Inclusive sum over the row's lanes.
+__device__ __forceinline__ int scan16i(int v) {
+  v += (int)dpp_shr<1>((uint32_t)v);
+  v += (int)dpp_shr<2>((uint32_t)v);
+  v += (int)dpp_shr<4>((uint32_t)v);
+  v += (int)dpp_shr<8>((uint32_t)v);
+  return v;
+}
 // Key of a score that is no NaN and no -0; from_ordered_key inverts it.
 __device__ __forceinline__ uint32_t score_key(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;  // of -inf
+
+// Moves and reductions of 64-bit values inside a 16-lane row.
+template <int kCtrl>
+__device__ __forceinline__ double dppd(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, ((uint64_t)dpp<kCtrl>((uint32_t)(b >> 32)) << 32) | dpp<kCtrl>((uint32_t)b));
+}
+__device__ __forceinline__ double sum16d(double v) {
+  v += dppd<kXor1>(v);
+  v += dppd<kXor2>(v);
+  v += dppd<kHalfMirror>(v);
+  v += dppd<kMirror>(v);
+  return v;
+}
+template <int kCtrl>
+__device__ __forceinline__ void top2_joind(double &a, double &b) {
+  const double c = dppd<kCtrl>(a), d = dppd<kCtrl>(b);
+  b = fmax(fmin(a, c), fmax(b, d));
+  a = fmax(a, c);
+}
+// A selection score in 64 bits (live experts; zd: the softmax's sum).
+__device__ __forceinline__ double wide_score(const GateArgs &g, float l, float m, double zd, int e) {
+  const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
+  const double p = exp(sigmoid ? -(double)l : (double)l - (double)m);
+  return (sigmoid ? 1.0 / (1.0 + p) : p / zd) + (g.bias ? (double)gate_logit(g.bias[e]) : 0.0);
+}
+// The softmax's sum over a row's experts in 64 bits.
+template <int kPer>
+__device__ __forceinline__ double wide_sum(const float (&l)[kPer], float m) {
+  double z = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    z += exp((double)l[i] - (double)m);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return sum16d(z);
+}
 
 // The two largest of a pair of lanes' two largest.
 template <int kCtrl>
@@ -264,12 +320,13 @@ __device__ __forceinline__ void top2_join(uint32_t &a, uint32_t &b) {
 // Number of other groups in the 16-lane row whose key comes before this lane's,
 // groups being `lanes` lanes wide; equal keys count where the other group is
 // the lower one (bit n of lower: the lane n places down the row).
-template <int N>
-__device__ __forceinline__ int groups_before(uint32_t key, uint32_t lower, int lanes) {
+template <int N, typename Key>
+__device__ __forceinline__ int groups_before(Key key, uint32_t lower, int lanes) {
   int before = 0;
   if constexpr (N < 16) {
     if ((N & (lanes - 1)) == 0) {  // uniform
-      const uint32_t other = dpp<0x120 + N>(key);  // row_ror
+      Key other = dpp<0x120 + N>((uint32_t)key);  // row_ror
+      if constexpr (sizeof(Key) == 8) other |= (Key)dpp<0x120 + N>((uint32_t)((uint64_t)key >> 32)) << 32;
       before = other > key - ((lower >> N) & 1u);
     }
     before += groups_before<N + 1>(key, lower, lanes);
@@ -357,7 +414,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       z = sum16(z);
     }
   }
-  // selection keys; 0: masked
+  // selection keys; 0: no expert of this lane
   uint32_t key[kPer];
   if (by_logit) {
 #pragma unroll
@@ -386,12 +443,12 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
         c[i] = gate_logit(c[i]) + __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = l[i] == -kInf ? 0u : score_key(c[i]);
+    for (int i = 0; i < kPer; ++i) key[i] = l[i] == -kInf ? kMaskedKey : score_key(c[i]);
   }
   uint32_t t1 = 0u, t2 = 0u;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    key[i] = key[i] <= kMaskedKey ? 0u : key[i];
+    if (!kFull) key[i] = i < a.count ? key[i] : 0u;
     t2 = max(t2, min(t1, key[i]));
     t1 = max(t1, key[i]);
   }
@@ -404,7 +461,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     uint32_t gk = k1;
     float size = 0.f;
     if (sums || !by_logit) {
-      float s1 = from_ordered_key(max(k1, kMaskedKey)), s2 = from_ordered_key(max(k2, kMaskedKey));
+      float s1 = from_ordered_key(k1), s2 = from_ordered_key(max(k2, kMaskedKey));
       if (by_logit) {  // the scores of the two logits (a softmax's without its common factor 1 / z)
         s1 = s1 == -kInf ? s1 : softmax ? expf(s1 - m) : 1.f / (1.f + expf(-s1));
         s2 = s2 == -kInf ? s2 : softmax ? expf(s2 - m) : 1.f / (1.f + expf(-s2));
@@ -414,49 +471,124 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       gk = score_key((sums ? s1 + s2 : s1) + 0.f);
     }
     kept = groups_before<1>(gk, a.lower, a.lanes) < g.topk_groups;
-    if (sums || !by_logit) {
+    if ((sums || !by_logit) && g.topk_groups < g.groups) {
       const float lo = from_ordered_key(min16_u32(kept ? gk : 0xFFFFFFFFu));
       const float hi = from_ordered_key(max16_u32(kept ? 0u : gk));
       // -inf on either side is exact (masked experts): the difference is then inf or NaN
-      unsure = g.topk_groups < g.groups && lo - hi <= 2.f * tol1 * (1.f + max16f(size));
+      const bool close = lo - hi <= 2.f * tol1 * (1.f + max16f(size));
+      if (__any(close)) {
+        // the 64-bit scores of the lane's two largest, which have to be its two
+        // largest for certain
+        int n = 0, e1 = 0, e2 = 0;
+        float l1 = -kInf, l2 = -kInf;
+        const float third = from_ordered_key(max(t2, kMaskedKey));
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i) {
+          const float v = from_ordered_key(max(key[i], kMaskedKey));
+          n += !by_logit && v > -kInf && v >= third - tol1 * (1.f + fabsf(third));
+          if (key[i] == t2 && key[i] != t1) { l2 = l[i]; e2 = a.e0 + i; }
+          if (key[i] == t1) {
+            // equal largest keys: the first and the one after it
+            if (t1 == t2) { l2 = l1; e2 = e1; }
+            l1 = l[i];
+            e1 = a.e0 + i;
+          }
+        }
+        const double zd = softmax && !by_logit ? wide_sum(l, m) : 1.0;
+        double d1 = -kInf, d2 = -kInf;
+        if (t1 > kMaskedKey) d1 = wide_score(g, l1, m, zd, e1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (t2 > kMaskedKey) d2 = wide_score(g, l2, m, zd, e2);
+        const double lane1 = fmax(d1, d2), lane2 = fmin(d1, d2);
+        d1 = lane1;
+        d2 = lane2;
+        if (a.lanes >= 2) top2_joind<kXor1>(d1, d2);
+        if (a.lanes >= 4) top2_joind<kXor2>(d1, d2);
+        if (a.lanes >= 8) top2_joind<kHalfMirror>(d1, d2);
+        const bool again = groups_before<1>(ordered_key64(sums ? d1 + d2 : d1), a.lower, a.lanes) < g.topk_groups;
+        kept = close ? again : kept;
+        unsure = close && n > 2;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) key[i] = kept ? key[i] : 0u;
   }
   t1 = kept ? t1 : 0u;
   t2 = kept ? t2 : 0u;
-  uint32_t tau = 0u;
+  // the least of the k largest of the lanes' two largest; with fewer than k of
+  // them every key counts
+  const bool enough = sum16i((t1 != 0u) + (t2 != 0u)) >= g.k;
+  uint32_t tau = 1u;
   for (int j = 0; j < g.k; ++j) {
-    tau = max16_u32(t1);
-    const bool out = t1 == tau;  // several lanes may go at once: tau only gets lower
+    const uint32_t most = max16_u32(t1);
+    tau = most != 0u ? most : tau;
+    const bool out = t1 == most;  // several lanes may go at once: tau only gets lower
     t1 = out ? t2 : t1;
     t2 = out ? 0u : t2;
   }
-  if (!by_logit && tau != 0u) {
-    const float v = from_ordered_key(tau);
-    tau = max(score_key((v - tol1 * (1.f + fabsf(v))) + 0.f), 1u);
-  }
-  int n = 0;
+  tau = enough ? tau : 1u;
+  // the least key a candidate may have: keys equal to tau are equal scores
+  // where they are exact
+  auto least = [&](uint32_t k0) {
+    const float v = from_ordered_key(k0);
+    return by_logit || k0 <= kMaskedKey ? k0 : score_key((v - tol1 * (1.f + fabsf(v))) + 0.f);
+  };
+  auto at_least = [&](uint32_t k0) {  // keys of this lane
+    int c = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) n += key[i] >= tau;
-  int pos = n;  // inclusive sum over the row's lanes
-  pos += (int)dpp_shr<1>(pos);
-  pos += (int)dpp_shr<2>(pos);
-  pos += (int)dpp_shr<4>(pos);
-  pos += (int)dpp_shr<8>(pos);
-  const int have = __shfl(pos, 15, 16);
-  pos -= n;
-  // tau 0: fewer than k live experts among the lanes' two largest
-  const bool fits = tau != 0u && have <= kFastK;
-  unsure |= !fits;
-  tau = fits ? tau : 0xFFFFFFFFu;  // no key is that large
+    for (int i = 0; i < kPer; ++i) c += key[i] >= k0;
+    return c;
+  };
+  uint32_t lo = least(tau);
+  int n = at_least(lo), have = sum16i(n);
+  if (__any(have > kFastK)) {
+    // too many for the lanes: tau goes up to the next key while k are left
+    bool more = have > kFastK;
+    while (__any(more)) {
+      uint32_t up = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) up = min(up, key[i] > tau ? key[i] : 0xFFFFFFFFu);
+      up = min16_u32(up);
+      more &= sum16i(at_least(up)) >= g.k;
+      tau = more ? up : tau;
+      lo = least(tau);
+      n = at_least(lo);
+      have = sum16i(n);
+      more &= have > kFastK;
+    }
+  }
+  const int pos0 = scan16i(n) - n;
   Candidates &cd = cands[row];
   wave_lds_fence();
   cd.key[li] = 0u;
   wave_lds_fence();
+  bool fits = have <= kFastK;
+  if (__any(!fits)) {
+    // equal scores at the end of the order: those above, then those equal to
+    // tau in expert order as far as there is room
+    const int above = at_least(tau + 1u), before = scan16i(above) - above, all = sum16i(above);
+    if (!fits) {
+      fits = (by_logit || tau <= kMaskedKey) && all < g.k;
+      have = kFastK;
+      int pa = before, pe = all + pos0 - before;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (fits && key[i] >= tau) {
+          const int p = key[i] > tau ? pa++ : pe++;
+          if (p < kFastK) {
+            cd.key[p] = key[i];
+            cd.l[p] = l[i];
+            cd.id[p] = a.e0 + i;
+          }
+        }
+      lo = 0xFFFFFFFFu;  // written, or left to the 64-bit gate: no key is that large
+    }
+  }
+  unsure |= !fits;
+  int pos = pos0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (key[i] >= tau) {
+    if (key[i] >= lo) {
       cd.key[pos] = key[i];
       cd.l[pos] = l[i];
       cd.id[pos] = a.e0 + i;
@@ -464,7 +596,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     }
   wave_lds_fence();
   const uint32_t ck = cd.key[li];  // 0: no candidate
-  const float cl = cd.l[li];
+  const float cl = ck <= kMaskedKey ? -kInf : cd.l[li];  // -inf: masked
   const int id = cd.id[li];
   int rank = 0;
 #pragma unroll
@@ -480,8 +612,22 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     wave_lds_fence();
     const int next = min(rank + 1, kFastK - 1);
     const float c = from_ordered_key(ck), d = from_ordered_key(cd.key[next]);
-    if (fits && rank + 1 < have && c - d <= tol1 * (1.f + fabsf(c)))
-      unsure |= cl != cd.l[next] || gate_logit(g.bias[id]) != gate_logit(g.bias[cd.id[next]]);
+    bool close = fits && ck > kMaskedKey && rank + 1 < have && c - d <= tol1 * (1.f + fabsf(c));
+    if (close) close = cl != cd.l[next] || gate_logit(g.bias[id]) != gate_logit(g.bias[cd.id[next]]);
+    if (__any(close)) {
+      // the candidates of the rows in question by 64-bit scores (equal ones in
+      // expert order)
+      const uint64_t rows = __ballot(close);
+      const double zd = softmax ? wide_sum(l, m) : 1.0;
+      const double s = ck > kMaskedKey ? wide_score(g, cl, m, zd, id) : -kInf;
+      const uint64_t wk = ck != 0u ? ordered_key64(s) : 0ull;
+      cd.wide[li] = wk;
+      cd.id[li] = id;
+      wave_lds_fence();
+      int again = 0;
+      for (int p = 0; p < kFastK; ++p) again += cd.wide[p] > wk || (cd.wide[p] == wk && cd.id[p] < id && wk != 0ull);
+      if ((rows >> (16 * row)) & 0xFFFFull) rank = again;
+    }
   }
   const uint64_t votes = __ballot(unsure && here);
   uint32_t redo = 0u;
