@@ -20,6 +20,7 @@
 namespace mq {
 
 constexpr float kInf = __builtin_inff();
+constexpr float kMost = 3.402823466e38f;  // the largest finite value
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Order-preserving map of a double to an unsigned integer; -0 maps to the key
@@ -33,7 +34,7 @@ __device__ __forceinline__ uint64_t ordered_key64(double v) {
 // A logit or a bias as the gate reads it: NaN counts as -inf (masked), +inf as
 // the largest finite value, -0 as +0.
 __device__ __forceinline__ float gate_logit(float v) {
-  return v == v ? fminf(v + 0.f, 3.402823466e38f) : -kInf;
+  return v == v ? fminf(v + 0.f, kMost) : -kInf;
 }
 __device__ __forceinline__ float load_gate_logit(const void *logits, int bf16, int64_t i) {
   return gate_logit(bf16 ? bf16_to_f32(((const uint16_t *)logits)[i]) : ((const float *)logits)[i]);
@@ -55,11 +56,21 @@ __device__ __forceinline__ float max64f(float v) {
 // renormalised); m and z: softmax maximum and sum over all experts.  Written so
 // that nothing overflows and small scores keep their digits: sigmoid(l) =
 // exp(min(l, 0)) / (1 + exp(-|l|)), a renormalised row shifted by its largest.
+// The hardware's exp2 and reciprocal are off by a unit in the last place, the
+// exponent by 2^-23 |l|: the weight by a few 2^-24 beside that.
 __device__ __forceinline__ float slot_score(const GateArgs &g, float l, float top, float m, float z) {
-  if (!(l > -kInf)) return 0.f;
-  if (g.score == MQ_SCORE_SIGMOID)
-    return expf(fminf(l, 0.f) - (g.renormalize ? fminf(top, 0.f) : 0.f)) / (1.f + expf(-fabsf(l)));
-  return g.renormalize ? expf(l - top) : expf(l - m) / z;
+  const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
+  const float down = sigmoid ? (g.renormalize ? fminf(top, 0.f) : 0.f) : g.renormalize ? top : m;
+  float s = __builtin_amdgcn_exp2f(((sigmoid ? fminf(l, 0.f) : l) - down) * kLog2e);
+  if (sigmoid)
+    s *= __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fabsf(l) * -kLog2e));
+  else if (!g.renormalize)
+    s *= __builtin_amdgcn_rcpf(z);
+  return l > -kInf ? s : 0.f;
+}
+// Divides by a row's sum (0 where every slot is masked).
+__device__ __forceinline__ float over_sum(float s, float sum) {
+  return sum > 0.f ? s * __builtin_amdgcn_rcpf(sum) : 0.f;
 }
 
 // The exponent of the power of two that brings a token's largest weight m into
@@ -191,7 +202,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
   float w = slot_score(g, lw, g.renormalize ? max64f(lw) : 0.f, m, (float)z);
   if (g.renormalize) {
     const float sum = sum64f(w);
-    w = sum > 0.f ? w / sum : 0.f;
+    w = over_sum(w, sum);
   }
   w *= g.scale;
   float down = 1.f;
@@ -396,8 +407,10 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       for (int i = 0; i < kPer; ++i) l[i] = i < a.count ? p[i] : -kInf;
     }
   }
+  if (by_logit || softmax) {  // a sigmoid's key below takes them as they are
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) l[i] = gate_logit(l[i]);
+    for (int i = 0; i < kPer; ++i) l[i] = gate_logit(l[i]);
+  }
 
   // softmax statistics, where a score or a weight needs them
   float m = 0.f, z = 1.f;
@@ -436,14 +449,16 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       const float zinv = 1.f / z;  // inf where every expert is masked: not used then
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        c[i] = gate_logit(c[i]) + __builtin_amdgcn_exp2f((l[i] - m) * kLog2e) * zinv;
+        c[i] += __builtin_amdgcn_exp2f((l[i] - m) * kLog2e) * zinv;
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        c[i] = gate_logit(c[i]) + __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
+        c[i] += __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
     }
+    // masked: a logit or a bias of -inf or NaN (a NaN is not greater than -inf)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = l[i] == -kInf ? kMaskedKey : score_key(c[i]);
+    for (int i = 0; i < kPer; ++i)
+      key[i] = l[i] > -kInf && c[i] > -kInf ? score_key(fminf(c[i], kMost)) : kMaskedKey;
   }
   uint32_t t1 = 0u, t2 = 0u;
 #pragma unroll
@@ -515,18 +530,20 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   }
   t1 = kept ? t1 : 0u;
   t2 = kept ? t2 : 0u;
-  // the least of the k largest of the lanes' two largest; with fewer than k of
-  // them every key counts
-  const bool enough = sum16i((t1 != 0u) + (t2 != 0u)) >= g.k;
-  uint32_t tau = 1u;
+  // the least of the k largest of the lanes' two largest
+  uint32_t tau = 0u, v1 = t1, v2 = t2;
   for (int j = 0; j < g.k; ++j) {
-    const uint32_t most = max16_u32(t1);
-    tau = most != 0u ? most : tau;
-    const bool out = t1 == most;  // several lanes may go at once: tau only gets lower
-    t1 = out ? t2 : t1;
-    t2 = out ? 0u : t2;
+    tau = max16_u32(v1);
+    const bool out = v1 == tau;  // several lanes may go at once: tau only gets lower
+    v1 = out ? v2 : v1;
+    v2 = out ? 0u : v2;
   }
-  tau = enough ? tau : 1u;
+  if (__any(tau == 0u)) {
+    // all of them went: their least, or every key where they are fewer than k
+    const uint32_t all = min16_u32(min(t1 ? t1 : 0xFFFFFFFFu, t2 ? t2 : 0xFFFFFFFFu));
+    const bool enough = sum16i((t1 != 0u) + (t2 != 0u)) >= g.k;
+    tau = tau != 0u ? tau : enough ? all : 1u;
+  }
   // the least key a candidate may have: keys equal to tau are equal scores
   // where they are exact
   auto least = [&](uint32_t k0) {
@@ -599,8 +616,14 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   const float cl = ck <= kMaskedKey ? -kInf : cd.l[li];  // -inf: masked
   const int id = cd.id[li];
   int rank = 0;
+  auto rank_among = [&](int first) {  // four candidates; equal keys: in expert order
 #pragma unroll
-  for (int p = 0; p < kFastK; ++p) rank += cd.key[p] > ck - (p < li ? 1u : 0u);  // equal keys: in expert order
+    for (int p = 0; p < 4; ++p) rank += cd.key[first + p] > ck - (first + p < li ? 1u : 0u);
+  };
+  rank_among(0);
+  rank_among(4);
+  if (__any(have > 8)) rank_among(8);
+  if (__any(have > 12)) rank_among(12);
   if (!by_logit) {
     // neighbours in the order, through LDS
     wave_lds_fence();
@@ -640,7 +663,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   float w = slot_score(g, sel ? cl : -kInf, top, m, z);
   if (g.renormalize) {
     const float sum = sum16(w);
-    w = sum > 0.f ? w / sum : 0.f;
+    w = over_sum(w, sum);
   }
   w *= g.scale;
   const bool done = here && !((redo >> row) & 1u);
