@@ -556,7 +556,7 @@ hipError_t launch_route(const LayerDims &L, const FwdPtrs &P, const Workspace &W
 
 bool route_groups(const LayerDims &L, const FwdPtrs &P, bool decode) {
   (void)L;
-  return !P.gated && decode && !P.w8a8 && P.act_g13 == 0.f && P.T <= kFusedT;
+  return decode && !P.w8a8 && P.act_g13 == 0.f && P.T <= kFusedT;
 }
 
 hipError_t launch_permute(const LayerDims &L, const FwdPtrs &P, const Workspace &W, bool decode,
