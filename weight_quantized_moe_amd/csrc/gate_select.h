@@ -81,8 +81,9 @@ __device__ __forceinline__ int weight_exponent(float m) {
   return ex < -120 ? -120 : ex > 120 ? 120 : ex;
 }
 
-// down: the power of two taken out of the weights (1 where none is).
-__device__ __forceinline__ void write_slot(const GateOut &o, int64_t at, int id, float w, float down) {
+// at: slot t k + j (below 2^28); down: the power of two taken out of the weights
+// (1 where none is).
+__device__ __forceinline__ void write_slot(const GateOut &o, uint32_t at, int id, float w, float down) {
   o.ids[at] = id;
   o.wts[at] = w * down;
   if (o.p_ids) o.p_ids[at] = id;
@@ -211,7 +212,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
     down = pow2f(-ex);
     if (lane == 0) o.wscale[t] = pow2f(ex);
   }
-  if (lane < g.k) write_slot(o, t * g.k + lane, slot_id, w, down);
+  if (lane < g.k) write_slot(o, (uint32_t)t * g.k + lane, slot_id, w, down);
 }
 
 // ---------------------------------------------------------------------------
@@ -371,15 +372,17 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   typedef uint32_t u2 __attribute__((ext_vector_type(2)));
   typedef f4 f4_a4 __attribute__((aligned(4)));
   const int li = lane & 15, row = lane >> 4;
-  const bool here = t0 + row < T;
-  const int64_t t = here ? t0 + row : T - 1;  // a row past the last token repeats it
+  const int rows = (int)min(T - t0, (int64_t)4);
+  const bool here = row < rows;
+  const int r = min(row, rows - 1);  // a row past the last token repeats it
+  const uint32_t t = (uint32_t)t0 + r;
   const GateLane a = gate_lane<kPer, kFull>(g, li);
   const bool softmax = g.score == MQ_SCORE_SOFTMAX, by_logit = g.bias == nullptr, sums = g.group_top == 2;
   const float tol1 = softmax ? 0x1p-17f : 0x1p-19f;
   float l[kPer];
-  const int64_t at = t * g.E + a.e0;
+  const uint32_t at = (uint32_t)(r * g.E + a.e0);  // from the wave's first logit on
   if (bf16) {
-    const uint16_t *p = (const uint16_t *)logits + at;
+    const uint16_t *p = (const uint16_t *)logits + t0 * g.E + at;
     if (kFull) {
       u2 u[kPer / 4];
 #pragma unroll
@@ -394,7 +397,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       for (int i = 0; i < kPer; ++i) l[i] = i < a.count ? bf16_to_f32(p[i]) : -kInf;
     }
   } else {
-    const float *p = (const float *)logits + at;
+    const float *p = (const float *)logits + t0 * g.E + at;
     if (kFull) {
 #pragma unroll
       for (int i = 0; i < kPer / 4; ++i) {
@@ -673,7 +676,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     down = pow2f(-ex);
     if (done && li == 0) o.wscale[t] = pow2f(ex);
   }
-  if (done && sel) write_slot(o, t * g.k + rank, id, w, down);
+  if (done && sel) write_slot(o, t * g.k + (uint32_t)rank, id, w, down);
   return redo;
 }
 
@@ -687,6 +690,7 @@ union GateLds {
 template <int kPer, bool kFull>
 __device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restrict__ logits, int bf16, int64_t t0,
                                           int64_t T, int lane, GateLds *lds, const GateOut &o) {
+  t0 = __builtin_amdgcn_readfirstlane((int)t0);  // the same in every lane: kept in scalar registers
   uint32_t redo = 0xFu;
   if constexpr (kPer > 0) redo = gate_tokens4<kPer, kFull>(g, logits, bf16, t0, T, lane, lds->cand, o);
   constexpr int kPer64 = kPer == 0 ? kMaxExperts / 64 : kPer <= 4 ? 1 : kPer / 4;
