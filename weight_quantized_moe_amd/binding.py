@@ -230,19 +230,32 @@ def _on_gpu(device, **tensors):
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+class _Quick:
+    """What the calls of the gate and the norm look up once: small calls are bound
+    by the host, so their checks take the form that costs the least, in front of
+    _need and _on_gpu (which name what is wrong)."""
+
+    def __init__(self):
+        import torch
+        self.device_now = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream     # of a GPU index
+        self.f32, self.bf16, self.i32, self.u8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+        self.on = torch.cuda.device
+
+
+_quick = None
+
+
+def _get_quick() -> _Quick:
+    global _quick
+    if _quick is None:
+        _quick = _Quick()
+    return _quick
+
+
 def _fits(t, shape, dtype, index) -> bool:
-    """Whether ``t`` is a contiguous tensor of this shape and dtype on GPU ``index``:
-    the checks of _need and _on_gpu in the form that costs the least, in front of
-    them (they name what is wrong).  Small calls are bound by the host."""
+    """Whether ``t`` is a contiguous tensor of this shape and dtype on GPU ``index``."""
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index
-
-
-def _raw_stream(stream, index) -> Optional[int]:
-    """The HIP stream of ``stream``, or of GPU ``index``'s current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -396,7 +409,7 @@ class Gate:
             _need(bias, "bias", (num_experts,), (torch.float32,))
             _on_gpu(None, bias=bias)
         self.num_experts, self.top_k, self.bias = num_experts, top_k, bias
-        self._f32, self._bf16, self._i32 = torch.float32, torch.bfloat16, torch.int32
+        self._q, self._call = _get_quick(), self._lib.moe_quant_gate_topk
         self._bias_index = None if bias is None else bias.get_device()
         self.desc = GateDesc(ABI_VERSION, num_experts, top_k, SCORES[score], num_groups, topk_groups,
                              group_top, int(renormalize), scale, _ptr(bias))
@@ -408,28 +421,29 @@ class Gate:
     def topk(self, logits, ids=None, weights=None, stream=None):
         """The gate of logits [T, E] (float32 or bfloat16): returns (ids int32
         [T, k], weights float32 [T, k])."""
-        import torch
+        q = self._q
         if logits.dim() != 2:
             raise ValueError("logits must be [T, E]")
-        t, k, index, dtype = logits.shape[0], self.top_k, logits.get_device(), logits.dtype
-        bf16 = dtype is self._bf16
-        if index >= 0 and index != torch.cuda.current_device():
-            with torch.cuda.device(index):
+        e, index, dtype = self.num_experts, logits.get_device(), logits.dtype
+        t = len(logits)
+        shape = (t, self.top_k)
+        if index >= 0 and index != q.device_now():
+            with q.on(index):
                 return self.topk(logits, ids, weights, stream)
-        shape = (t, k)
         if ids is None:
-            ids = _empty(shape, torch.int32, logits.device, stream)
+            ids = _empty(shape, q.i32, logits.device, stream)
         if weights is None:
-            weights = _empty(shape, torch.float32, logits.device, stream)
-        if not (index >= 0 and _fits(logits, (t, self.num_experts), self._bf16 if bf16 else self._f32, index)
-                and _fits(ids, shape, self._i32, index) and _fits(weights, shape, self._f32, index)
-                and self._bias_index in (None, index)):
-            _need(logits, "logits", (t, self.num_experts), (torch.float32, torch.bfloat16))
-            _need(ids, "ids", shape, (torch.int32,))
-            _need(weights, "weights", shape, (torch.float32,))
+            weights = _empty(shape, q.f32, logits.device, stream)
+        if not (index >= 0 and (dtype is q.f32 or dtype is q.bf16) and logits.shape[1] == e and logits.is_contiguous()
+                and ids.dtype is q.i32 and ids.shape == shape and ids.is_contiguous() and ids.get_device() == index
+                and weights.dtype is q.f32 and weights.shape == shape and weights.is_contiguous()
+                and weights.get_device() == index and self._bias_index in (None, index)):
+            _need(logits, "logits", (t, e), (q.f32, q.bf16))
+            _need(ids, "ids", shape, (q.i32,))
+            _need(weights, "weights", shape, (q.f32,))
             _on_gpu(logits.device, logits=logits, bias=self.bias, ids=ids, weights=weights)
-        st = self._lib.moe_quant_gate_topk(self._ref, logits.data_ptr(), MQ_BF16 if bf16 else MQ_F32, t, ids.data_ptr(),
-                                           weights.data_ptr(), _raw_stream(stream, index))
+        st = self._call(self._ref, logits.data_ptr(), MQ_F32 if dtype is q.f32 else MQ_BF16, t, ids.data_ptr(),
+                        weights.data_ptr(), q.raw_stream(index) if stream is None else stream.cuda_stream)
         if st:
             _check(self._lib, st)
         return ids, weights
@@ -462,7 +476,7 @@ class ResidualNorm:
         _on_gpu(None, post_weight=post_weight, pre_weight=pre_weight)
         self.hidden, self.residual_dtype = hidden, residual_dtype
         self.post_weight, self.pre_weight = post_weight, pre_weight
-        self._bf16, self._types = torch.bfloat16, types
+        self._types, self._q, self._call = types, _get_quick(), self._lib.moe_quant_norm
         self._index = {w.get_device() for w in (post_weight, pre_weight) if w is not None}
         self.desc = NormDesc(ABI_VERSION, hidden, _mq_dtype(residual_dtype), _mq_dtype(weight_dtype), eps,
                              weight_offset, scale, _ptr(post_weight), _ptr(pre_weight))
@@ -476,15 +490,15 @@ class ResidualNorm:
         float32 or bfloat16: [H] per channel, [T, 1] per token or [T, H].
         Returns (residual_out, norm_out); norm_out is None without a
         ``pre_weight``.  The outputs may be the inputs' own buffers."""
-        import torch
+        q = self._q
         first = x if x is not None else residual
         if first is None or first.dim() != 2:
             raise ValueError("need x or residual [T, H]")
-        t, h, index = first.shape[0], self.hidden, first.get_device()
-        if index >= 0 and index != torch.cuda.current_device():
-            with torch.cuda.device(index):
+        t, h, index = len(first), self.hidden, first.get_device()
+        if index >= 0 and index != q.device_now():
+            with q.on(index):
                 return self.forward(x, residual, gate, residual_out, norm_out, stream)
-        shape, rd = (t, h), self.residual_dtype
+        shape, rd, bf16 = (t, h), self.residual_dtype, q.bf16
         kind, gate_dtype, gate_ptr = GATE_NONE, MQ_F32, None
         if gate is not None:
             gs = gate.shape
@@ -498,26 +512,26 @@ class ResidualNorm:
             if norm_out is not None:
                 raise ValueError("norm_out needs a pre_weight")
         elif norm_out is None:
-            norm_out = _empty(shape, self._bf16, first.device, stream)
-        if not (index >= 0 and (x is None or _fits(x, shape, self._bf16, index))
+            norm_out = _empty(shape, bf16, first.device, stream)
+        if not (index >= 0 and (x is None or _fits(x, shape, bf16, index))
                 and (residual is None or _fits(residual, shape, rd, index)) and _fits(residual_out, shape, rd, index)
-                and (norm_out is None or _fits(norm_out, shape, self._bf16, index)) and self._index <= {index}
+                and (norm_out is None or _fits(norm_out, shape, bf16, index)) and self._index <= {index}
                 and (gate is None or gate.dtype in self._types and _fits(gate, gs, gate.dtype, index))):
             if x is not None:
-                _need(x, "x", shape, (torch.bfloat16,))
+                _need(x, "x", shape, (bf16,))
             if residual is not None:
                 _need(residual, "residual", shape, (rd,))
             if gate is not None:
                 _need(gate, "gate", tuple(gs), self._types)
             _need(residual_out, "residual_out", shape, (rd,))
             if norm_out is not None:
-                _need(norm_out, "norm_out", shape, (torch.bfloat16,))
+                _need(norm_out, "norm_out", shape, (bf16,))
             _on_gpu(first.device, x=x, residual=residual, gate=gate, residual_out=residual_out, norm_out=norm_out,
                     post_weight=self.post_weight, pre_weight=self.pre_weight)
-        st = self._lib.moe_quant_norm(
+        st = self._call(
             self._ref, None if x is None else x.data_ptr(), None if residual is None else residual.data_ptr(), gate_ptr,
             kind, gate_dtype, t, residual_out.data_ptr(), None if norm_out is None else norm_out.data_ptr(),
-            _raw_stream(stream, index))
+            q.raw_stream(index) if stream is None else stream.cuda_stream)
         if st:
             _check(self._lib, st)
         return residual_out, norm_out
@@ -637,7 +651,7 @@ class Layer:
         ``logits`` or from the router weight ``router_w`` [E, H]; ``activations``:
         "bf16", "fp8" (FP8 layers) or "nvfp4" (NVFP4 layers, with the calibrated
         global scales)."""
-        import torch
+        q = gate._q
         if (logits is None) == (router_w is None):
             raise ValueError("forward_gated needs exactly one of logits and router_w")
         if activations not in ACTIVATIONS:
@@ -646,9 +660,9 @@ class Layer:
             raise ValueError("logits_out needs router_w")
         if hidden.dim() != 2:
             raise ValueError("hidden must be [T, H]")
-        index, t, bf16 = hidden.get_device(), hidden.shape[0], torch.bfloat16
-        if index >= 0 and index != torch.cuda.current_device():
-            with torch.cuda.device(index):
+        index, t, bf16 = hidden.get_device(), len(hidden), q.bf16
+        if index >= 0 and index != q.device_now():
+            with q.on(index):
                 return self.forward_gated(gate, hidden, logits, router_w, residual, out, workspace, activations,
                                           act_gscale13, act_gscale2, logits_out, probe, events, stream)
         if gate.bias is not None and gate.bias.device != self.device:
@@ -656,13 +670,13 @@ class Layer:
         if out is None:
             out = _empty((t, self.hidden), bf16, self.device, stream)
         if workspace is None:
-            workspace = _empty((max(self.workspace_size(t), 256),), torch.uint8, self.device, stream)
+            workspace = _empty((max(self.workspace_size(t), 256),), q.u8, self.device, stream)
         shape, wide = (t, self.hidden), logits_out if logits is None else logits
         if (probe is None and events is None and index == self.device.index and t > 0
                 and _fits(hidden, shape, bf16, index) and _fits(out, shape, bf16, index)
                 and (residual is None or _fits(residual, shape, bf16, index))
                 and (router_w is None or _fits(router_w, (self.num_experts, self.hidden), bf16, index))
-                and (wide is None or _fits(wide, (t, self.num_experts), torch.float32, index)
+                and (wide is None or _fits(wide, (t, self.num_experts), q.f32, index)
                      or (logits is not None and _fits(logits, (t, self.num_experts), bf16, index)))
                 and workspace.is_contiguous() and workspace.get_device() == index
                 and _nbytes(workspace) >= self._workspace_need(t)):
@@ -671,7 +685,7 @@ class Layer:
                 self._h, gate._ref, _ptr(logits), MQ_BF16 if logits is not None and logits.dtype is bf16 else MQ_F32,
                 _ptr(router_w), hidden.data_ptr(), _ptr(residual), t, out.data_ptr(), workspace.data_ptr(),
                 _nbytes(workspace), ACTIVATIONS[activations], act_gscale13, act_gscale2, _ptr(logits_out), None,
-                _raw_stream(stream, index))
+                q.raw_stream(index) if stream is None else stream.cuda_stream)
             if st:
                 _check(self._lib, st)
             return out
