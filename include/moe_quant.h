@@ -434,7 +434,8 @@ mq_status moe_quant_forward_gated(const mq_layer *L, const mq_gate *gate, const 
  * (the layer's, for instance), n the next block's input.  n is computed from
  * the rounded r', so one call gives the same bits as two (x and post_weight
  * first, then residual = r' and pre_weight).  Squares are summed in FP32:
- * values beyond 2^55 in magnitude are outside of this entry's range.
+ * values beyond 2^55 in magnitude are outside of this entry's range (eps covers
+ * what small squares lose).
  */
 typedef enum {
   MQ_GATE_NONE = 0,
@@ -448,7 +449,7 @@ typedef struct {
   int32_t hidden;         /* H, 1 to 32768                                  */
   int32_t residual_dtype; /* mq_dtype of residual and residual_out          */
   int32_t weight_dtype;   /* mq_dtype of post_weight and pre_weight         */
-  float eps;              /* finite and positive                            */
+  float eps;              /* finite and at least 1e-30                      */
   float weight_offset;    /* finite: 0, or 1 where weights are stored as w - 1 */
   float scale;            /* finite                                         */
   const void *post_weight;/* NULL (no norm after the block) or [H]          */

@@ -104,7 +104,7 @@ def _norm(**over):
 
 @pytest.mark.parametrize("over,args,expect", [
     (dict(abi=0), {}, ABI), (dict(h=0), {}, SHAPE), (dict(h=32769), {}, SHAPE), (dict(rd=2), {}, DTYPE),
-    (dict(wd=-1), {}, DTYPE), (dict(eps=0.0), {}, SHAPE), (dict(eps=-1.0), {}, SHAPE), (dict(eps=math.nan), {}, SHAPE),
+    (dict(wd=-1), {}, DTYPE), (dict(eps=0.0), {}, SHAPE), (dict(eps=1e-31), {}, SHAPE), (dict(eps=-1.0), {}, SHAPE), (dict(eps=math.nan), {}, SHAPE),
     (dict(off=math.inf), {}, SHAPE), (dict(scale=math.nan), {}, SHAPE), ({}, dict(kind=4, gate=P), SHAPE),
     ({}, dict(kind=-1), SHAPE), ({}, dict(kind=1, gate=P, gd=7), DTYPE), ({}, dict(t=-1), SHAPE),
     ({}, dict(t=(1 << 22) + 1), SHAPE), ({}, dict(gate=P), NULL), ({}, dict(kind=2), NULL), ({}, dict(x=None), NULL),

@@ -21,7 +21,7 @@ struct StageArgs {
   uint32_t *flags;
   float act_g;
 };
-template <int kPer, bool kFull>
+template <int kPer, GateMode kMode>
 __global__ __launch_bounds__(256) void gate_stage_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                          GateOut o, StageArgs a) {
   __shared__ GateLds lds[4];
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void gate_stage_kernel(GateArgs g, const void 
   if (blockIdx.x == 0 && threadIdx.x == 0) a.flags[0] = 0u;
   if ((int)blockIdx.x < a.gate_blocks) {
     const int64_t t0 = ((int64_t)blockIdx.x * waves + wave) * 4;
-    if (t0 < a.T) gate_wave<kPer, kFull>(g, logits, bf16, t0, a.T, lane, &lds[wave], o);
+    if (t0 < a.T) gate_wave<kPer, kMode>(g, logits, bf16, t0, a.T, lane, &lds[wave], o);
     return;
   }
   const int t0 = (((int)blockIdx.x - a.gate_blocks) * waves + wave) * 4, T = a.T, H = a.H;
@@ -55,7 +55,7 @@ struct GroupArgs {
   int4 *rowinfo;
   int32_t *inv_pos, *p_offsets, *p_sorted_tok, *p_inv;
 };
-template <int kPer, bool kFull>
+template <int kPer, GateMode kMode>
 __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                          GateOut o, StageArgs a, GroupArgs q) {
   __shared__ GateLds lds[4];
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void 
   if (t0 < a.T) {
     if (wave < 4) {
       const GateOut in_lds = {s_ids, s_wts, o.wscale, o.p_ids, o.p_w};
-      gate_wave<kPer, kFull>(g, logits, bf16, t0, a.T, lane, &lds[wave], in_lds);
+      gate_wave<kPer, kMode>(g, logits, bf16, t0, a.T, lane, &lds[wave], in_lds);
     } else if (a.stage_rows == 2) {
       u4 v[4][4];
 #pragma unroll
@@ -112,16 +112,16 @@ hipError_t launch_route_gated(const LayerDims &L, const FwdPtrs &P, const Worksp
     const GroupArgs q = {(int32_t *)(ws + W.offsets), (int32_t *)(ws + W.mtile), (int4 *)(ws + W.active),
                          (int32_t *)(ws + W.rcpre), (int32_t *)(ws + W.sorted_slots), (int4 *)(ws + W.rowinfo),
                          (int32_t *)(ws + W.inv_pos), P.p_offsets, P.p_sorted_tok, P.p_inv};
-    return with_gate_variant(*P.gated, [&](auto per, auto full) {
-      hipLaunchKernelGGL((gate_group_kernel<per(), full()>), dim3(1), dim3(512), 0, s, *P.gated, logits, bf16, o, a, q);
+    return with_gate_variant<false>(*P.gated, [&](auto per, auto mode) {
+      hipLaunchKernelGGL((gate_group_kernel<per(), mode()>), dim3(1), dim3(512), 0, s, *P.gated, logits, bf16, o, a, q);
       return hipGetLastError();
     });
   }
-  return with_gate_variant(*P.gated, [&](auto per, auto full) {
+  return with_gate_variant<false>(*P.gated, [&](auto per, auto mode) {
     const int threads = P.T <= 4096 ? 64 : 256, tpb = threads / 16;
     a.gate_blocks = (P.T + tpb - 1) / tpb;
     const unsigned blocks = (unsigned)a.gate_blocks * (stage_rows ? 2u : 1u);
-    hipLaunchKernelGGL((gate_stage_kernel<per(), full()>), dim3(blocks), dim3(threads), 0, s, *P.gated, logits, bf16, o, a);
+    hipLaunchKernelGGL((gate_stage_kernel<per(), mode()>), dim3(blocks), dim3(threads), 0, s, *P.gated, logits, bf16, o, a);
     return hipGetLastError();
   });
 }

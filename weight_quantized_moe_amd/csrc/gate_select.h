@@ -228,8 +228,9 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
 //      in expert order;
 //   4. each lane ranks the candidate it holds by counting those before it.
 // What is not certain at 32 bits: a score is off by at most 2^-22 + 2^-24 |c|
-// for a sigmoid (exponent 2^-23 |l| s(1 - s) <= 2^-25, reciprocal and sums) and
-// 2^-19 + 2^-24 |c| for a softmax (its sum over 512 experts, 32 a lane), so two
+// for a sigmoid (exponent 2^-23 |l| s(1 - s) <= 2^-25, reciprocal and sums), and
+// for a softmax by 2^-22 + 2^-24 |c| and a common factor 1 + 2^-18 (its sum: at
+// most 35 additions, 32 experts a lane, and the terms' own errors), so two
 // scores further apart than tol = 2^-19 (1 + |c|), for a softmax 2^-17 (1 +
 // |c|), are in their order.  tau is lowered by tol.  Where two candidates next
 // to each other in the order are within tol and not the same logit and bias,
@@ -352,20 +353,26 @@ struct GateLane {
   int e0, count;   // first expert of this lane, and how many
   uint32_t lower;  // bit n: the lane n places down the row is of a lower group
 };
-template <int kPer, bool kFull>
+template <int kPer, bool kWhole>
 __device__ __forceinline__ GateLane gate_lane(const GateArgs &g, int li) {
   GateLane a;
   const int shift = 4 - (31 - __builtin_clz(g.groups));
   a.lanes = 1 << shift;
   const int off = li & (a.lanes - 1);
-  const int chunk = kFull ? kPer : (g.per + a.lanes - 1) >> shift;
-  a.e0 = kFull ? li * kPer : (li >> shift) * g.per + off * chunk;
-  a.count = kFull ? kPer : max(0, min(chunk, g.per - off * chunk));
+  const int chunk = kWhole ? kPer : (g.per + a.lanes - 1) >> shift;
+  a.e0 = kWhole ? li * kPer : (li >> shift) * g.per + off * chunk;
+  a.count = kWhole ? kPer : max(0, min(chunk, g.per - off * chunk));
   a.lower = ((2u << li) - 1u) & ~((2u << off) - 1u);
   return a;
 }
 
-template <int kPer, bool kFull>
+// What of a gate is fixed when a kernel is compiled.  kAny: nothing; kFull: each
+// lane holds kPer experts (E = 16 kPer), loaded 16 bytes at a time; the others:
+// that, the source of the order (logits, sigmoid or softmax plus bias), and
+// whether there are groups.  Branches on these took a fifth of the kernel.
+enum GateMode { kAny, kFull, kLogits, kSigmoid, kSoftmax, kLogitsGroups, kSigmoidGroups, kSoftmaxGroups };
+
+template <int kPer, GateMode kMode>
 __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *__restrict__ logits, int bf16,
                                                  int64_t t0, int64_t T, int lane, Candidates *cands,
                                                  const GateOut &o) {
@@ -376,14 +383,20 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   const bool here = row < rows;
   const int r = min(row, rows - 1);  // a row past the last token repeats it
   const uint32_t t = (uint32_t)t0 + r;
-  const GateLane a = gate_lane<kPer, kFull>(g, li);
-  const bool softmax = g.score == MQ_SCORE_SOFTMAX, by_logit = g.bias == nullptr, sums = g.group_top == 2;
+  constexpr bool kWhole = kMode != kAny, kFixed = kMode > kFull;
+  constexpr bool kByLogit = kMode == kLogits || kMode == kLogitsGroups;
+  constexpr bool kGroups = kMode >= kLogitsGroups;
+  const GateLane a = gate_lane<kPer, kWhole>(g, li);
+  const bool by_logit = kFixed ? kByLogit : g.bias == nullptr, groups = kFixed ? kGroups : g.groups > 1;
+  const bool softmax = kFixed && !kByLogit ? kMode == kSoftmax || kMode == kSoftmaxGroups
+                                           : g.score == MQ_SCORE_SOFTMAX;
+  const bool sums = groups && g.group_top == 2;
   const float tol1 = softmax ? 0x1p-17f : 0x1p-19f;
   float l[kPer];
   const uint32_t at = (uint32_t)(r * g.E + a.e0);  // from the wave's first logit on
   if (bf16) {
     const uint16_t *p = (const uint16_t *)logits + t0 * g.E + at;
-    if (kFull) {
+    if (kWhole) {
       u2 u[kPer / 4];
 #pragma unroll
       for (int i = 0; i < kPer / 4; ++i) u[i] = *(const u2 *)(p + 4 * i);
@@ -398,10 +411,10 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     }
   } else {
     const float *p = (const float *)logits + t0 * g.E + at;
-    if (kFull) {
+    if (kWhole) {
 #pragma unroll
       for (int i = 0; i < kPer / 4; ++i) {
-        const f4 u = *(const f4 *)(p + 4 * i);
+        const f4 u = *(const f4_a4 *)(p + 4 * i);  // logits computed here may be aligned to 4 bytes
 #pragma unroll
         for (int q = 0; q < 4; ++q) l[4 * i + q] = u[q];
       }
@@ -437,7 +450,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     for (int i = 0; i < kPer; ++i) key[i] = score_key(l[i]);
   } else {
     float c[kPer];
-    if (kFull) {
+    if (kWhole) {
 #pragma unroll
       for (int i = 0; i < kPer / 4; ++i) {
         const f4 u = *(const f4_a4 *)(g.bias + a.e0 + 4 * i);
@@ -466,12 +479,12 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   uint32_t t1 = 0u, t2 = 0u;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (!kFull) key[i] = i < a.count ? key[i] : 0u;
+    if (!kWhole) key[i] = i < a.count ? key[i] : 0u;
     t2 = max(t2, min(t1, key[i]));
     t1 = max(t1, key[i]);
   }
   bool unsure = false, kept = true;
-  if (g.groups > 1) {
+  if (groups) {
     uint32_t k1 = t1, k2 = t2;
     if (a.lanes >= 2) top2_join<kXor1>(k1, k2);
     if (a.lanes >= 4) top2_join<kXor2>(k1, k2);
@@ -687,27 +700,41 @@ union GateLds {
   Candidates cand[4];
   double sc[kMaxExperts];
 };
-template <int kPer, bool kFull>
+template <int kPer, GateMode kMode>
 __device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restrict__ logits, int bf16, int64_t t0,
                                           int64_t T, int lane, GateLds *lds, const GateOut &o) {
   t0 = __builtin_amdgcn_readfirstlane((int)t0);  // the same in every lane: kept in scalar registers
   uint32_t redo = 0xFu;
-  if constexpr (kPer > 0) redo = gate_tokens4<kPer, kFull>(g, logits, bf16, t0, T, lane, lds->cand, o);
+  if constexpr (kPer > 0) redo = gate_tokens4<kPer, kMode>(g, logits, bf16, t0, T, lane, lds->cand, o);
   constexpr int kPer64 = kPer == 0 ? kMaxExperts / 64 : kPer <= 4 ? 1 : kPer / 4;
   for (int r = 0; r < 4 && t0 + r < T; ++r)
     if ((redo >> r) & 1u) gate_token<kPer64>(g, logits, bf16, t0 + r, lane, lds->sc, o);
 }
 
-// Calls f with the kernel variant for this gate: f(kPer, kFull) as constants.
-template <typename F>
+// Calls f with the kernel variant for this gate: f(kPer, mode) as constants.
+// kFixed: with the modes beyond kFull.
+template <bool kFixed, typename F>
 static hipError_t with_gate_variant(const GateArgs &g, F f) {
   using std::integral_constant;
   const int lanes = 16 / g.groups;  // 0 above 16 groups
-  if (g.k > kFastK || lanes == 0 || 16 % g.groups) return f(integral_constant<int, 0>{}, integral_constant<bool, false>{});
+  if (g.k > kFastK || lanes == 0 || 16 % g.groups)
+    return f(integral_constant<int, 0>{}, integral_constant<GateMode, kAny>{});
   const int chunk = (g.per + lanes - 1) / lanes;
   const bool full = chunk * 16 == g.E;
   auto go = [&](auto n) {
-    return full && chunk == n() ? f(n, integral_constant<bool, true>{}) : f(n, integral_constant<bool, false>{});
+    if (!full || chunk != n()) return f(n, integral_constant<GateMode, kAny>{});
+    if constexpr (kFixed) {
+      const bool groups = g.groups > 1;
+      if (!g.bias)
+        return groups ? f(n, integral_constant<GateMode, kLogitsGroups>{}) : f(n, integral_constant<GateMode, kLogits>{});
+      if (g.score == MQ_SCORE_SIGMOID)
+        return groups ? f(n, integral_constant<GateMode, kSigmoidGroups>{})
+                      : f(n, integral_constant<GateMode, kSigmoid>{});
+      return groups ? f(n, integral_constant<GateMode, kSoftmaxGroups>{})
+                    : f(n, integral_constant<GateMode, kSoftmax>{});
+    } else {
+      return f(n, integral_constant<GateMode, kFull>{});
+    }
   };
   if (chunk <= 4) return go(integral_constant<int, 4>{});
   if (chunk <= 8) return go(integral_constant<int, 8>{});

@@ -7,21 +7,21 @@
 
 namespace mq {
 
-template <int kPer, bool kFull>
+template <int kPer, GateMode kMode>
 __global__ __launch_bounds__(256) void gate_topk_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                         int64_t T, GateOut o) {
   __shared__ GateLds lds[4];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t t0 = ((int64_t)blockIdx.x * (blockDim.x >> 6) + wave) * 4;
-  if (t0 < T) gate_wave<kPer, kFull>(g, logits, bf16, t0, T, lane, &lds[wave], o);
+  if (t0 < T) gate_wave<kPer, kMode>(g, logits, bf16, t0, T, lane, &lds[wave], o);
 }
 
 hipError_t launch_gate_topk(const GateArgs &g, const void *logits, int bf16, int64_t T, const GateOut &o,
                             hipStream_t s) {
-  return with_gate_variant(g, [&](auto per, auto full) {
+  return with_gate_variant<true>(g, [&](auto per, auto mode) {
     // one wave a workgroup spreads a small batch over the CUs
     const int threads = T <= 4096 ? 64 : 256, tpb = threads / 16;
-    hipLaunchKernelGGL((gate_topk_kernel<per(), full()>), dim3((unsigned)((T + tpb - 1) / tpb)), dim3(threads), 0, s, g,
+    hipLaunchKernelGGL((gate_topk_kernel<per(), mode()>), dim3((unsigned)((T + tpb - 1) / tpb)), dim3(threads), 0, s, g,
                        logits, bf16, T, o);
     return hipGetLastError();
   });

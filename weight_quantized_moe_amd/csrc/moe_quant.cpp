@@ -472,8 +472,8 @@ mq_status moe_quant_norm(const mq_norm *n, const uint16_t *x_bf16, const void *r
       (gate_kind != MQ_GATE_NONE && !known_dtype(gate_dtype)))
     return fail(MQ_E_DTYPE, "norm: unknown residual, weight or gate dtype (%d, %d, %d)", n->residual_dtype,
                 n->weight_dtype, gate_dtype);
-  if (!std::isfinite(n->eps) || !(n->eps > 0.f))
-    return fail(MQ_E_SHAPE, "norm: eps %g must be finite and positive", (double)n->eps);
+  if (!std::isfinite(n->eps) || !(n->eps >= 1e-30f))
+    return fail(MQ_E_SHAPE, "norm: eps %g must be finite and at least 1e-30", (double)n->eps);
   if (!std::isfinite(n->weight_offset) || !std::isfinite(n->scale))
     return fail(MQ_E_SHAPE, "norm: weight_offset %g and scale %g must be finite", (double)n->weight_offset,
                 (double)n->scale);
