@@ -360,7 +360,7 @@ __device__ __forceinline__ GateLane gate_lane(const GateArgs &g, int li) {
   a.lanes = 1 << shift;
   const int off = li & (a.lanes - 1);
   const int chunk = kWhole ? kPer : (g.per + a.lanes - 1) >> shift;
-  a.e0 = kWhole ? li * kPer : (li >> shift) * g.per + off * chunk;
+  a.e0 = kWhole ? li * kPer : min((li >> shift) * g.per + off * chunk, g.E);
   a.count = kWhole ? kPer : max(0, min(chunk, g.per - off * chunk));
   a.lower = ((2u << li) - 1u) & ~((2u << off) - 1u);
   return a;
@@ -392,6 +392,11 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
                                            : g.score == MQ_SCORE_SOFTMAX;
   const bool sums = groups && g.group_top == 2;
   const float tol1 = softmax ? 0x1p-17f : 0x1p-19f;
+  // without whole lanes: what a lane loads beyond its experts is some other
+  // logit, and its key is 0; only the array's end must not be passed
+  const int64_t left = (T - t0) * g.E;  // logits from the wave's first on
+  const bool inside = left >= 4 * g.E + kPer;
+  const uint32_t last = (uint32_t)min(left - 1, (int64_t)0x7FFFFFFF);
   float l[kPer];
   const uint32_t at = (uint32_t)(r * g.E + a.e0);  // from the wave's first logit on
   if (bf16) {
@@ -405,9 +410,12 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
         const uint32_t w = u[i / 4][(i >> 1) & 1];
         l[i] = __builtin_bit_cast(float, i & 1 ? w & 0xFFFF0000u : w << 16);
       }
+    } else if (inside) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) l[i] = bf16_to_f32(p[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) l[i] = i < a.count ? bf16_to_f32(p[i]) : -kInf;
+      for (int i = 0; i < kPer; ++i) l[i] = bf16_to_f32(((const uint16_t *)logits + t0 * g.E)[min(at + i, last)]);
     }
   } else {
     const float *p = (const float *)logits + t0 * g.E + at;
@@ -418,14 +426,17 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
 #pragma unroll
         for (int q = 0; q < 4; ++q) l[4 * i + q] = u[q];
       }
+    } else if (inside) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) l[i] = p[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) l[i] = i < a.count ? p[i] : -kInf;
+      for (int i = 0; i < kPer; ++i) l[i] = ((const float *)logits + t0 * g.E)[min(at + i, last)];
     }
   }
   if (by_logit || softmax) {  // a sigmoid's key below takes them as they are
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) l[i] = gate_logit(l[i]);
+    for (int i = 0; i < kPer; ++i) l[i] = kWhole || i < a.count ? gate_logit(l[i]) : -kInf;
   }
 
   // softmax statistics, where a score or a weight needs them
@@ -459,7 +470,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) c[i] = i < a.count ? g.bias[a.e0 + i] : -kInf;
+      for (int i = 0; i < kPer; ++i) c[i] = g.bias[min(a.e0 + i, g.E - 1)];
     }
     if (softmax) {
       const float zinv = 1.f / z;  // inf where every expert is masked: not used then
