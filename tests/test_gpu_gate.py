@@ -85,7 +85,7 @@ KINDS = {
 @pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("with_bias", [False, True])
 @pytest.mark.parametrize("t,e,k", [(1, 1, 1), (1, 128, 8), (2, 7, 7), (5, 16, 4), (17, 65, 3), (64, 127, 16),
-                                   (33, 128, 17), (130, 256, 8), (7, 511, 64), (300, 72, 6), (3, 512, 33)])
+                                   (33, 128, 17), (130, 256, 8), (7, 511, 64), (300, 72, 6), (3, 512, 33), (37, 192, 8), (37, 384, 8), (9, 380, 16), (21, 186, 5), (5, 2, 1)])
 def test_topk(kind, with_bias, t, e, k):
     check(logits(t, e, seed=t + e), k, bias=a_bias(e) if with_bias else None, **KINDS[kind])
 

@@ -749,7 +749,9 @@ static hipError_t with_gate_variant(const GateArgs &g, F f) {
   };
   if (chunk <= 4) return go(integral_constant<int, 4>{});
   if (chunk <= 8) return go(integral_constant<int, 8>{});
+  if (chunk <= 12) return go(integral_constant<int, 12>{});
   if (chunk <= 16) return go(integral_constant<int, 16>{});
+  if (chunk <= 24) return go(integral_constant<int, 24>{});
   return go(integral_constant<int, 32>{});
 }
 
