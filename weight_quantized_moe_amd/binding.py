@@ -421,11 +421,10 @@ class Gate:
     def topk(self, logits, ids=None, weights=None, stream=None):
         """The gate of logits [T, E] (float32 or bfloat16): returns (ids int32
         [T, k], weights float32 [T, k])."""
-        q = self._q
-        if logits.dim() != 2:
+        q, given, index, dtype = self._q, logits.shape, logits.get_device(), logits.dtype
+        if len(given) != 2:
             raise ValueError("logits must be [T, E]")
-        e, index, dtype = self.num_experts, logits.get_device(), logits.dtype
-        t = len(logits)
+        t, e = given[0], self.num_experts
         shape = (t, self.top_k)
         if index >= 0 and index != q.device_now():
             with q.on(index):
@@ -434,7 +433,7 @@ class Gate:
             ids = _empty(shape, q.i32, logits.device, stream)
         if weights is None:
             weights = _empty(shape, q.f32, logits.device, stream)
-        if not (index >= 0 and (dtype is q.f32 or dtype is q.bf16) and logits.shape[1] == e and logits.is_contiguous()
+        if not (index >= 0 and (dtype is q.f32 or dtype is q.bf16) and given[1] == e and logits.is_contiguous()
                 and ids.dtype is q.i32 and ids.shape == shape and ids.is_contiguous() and ids.get_device() == index
                 and weights.dtype is q.f32 and weights.shape == shape and weights.is_contiguous()
                 and weights.get_device() == index and self._bias_index in (None, index)):
@@ -477,7 +476,7 @@ class ResidualNorm:
         self.hidden, self.residual_dtype = hidden, residual_dtype
         self.post_weight, self.pre_weight = post_weight, pre_weight
         self._types, self._q, self._call = types, _get_quick(), self._lib.moe_quant_norm
-        self._index = {w.get_device() for w in (post_weight, pre_weight) if w is not None}
+        self._index = frozenset(w.get_device() for w in (post_weight, pre_weight) if w is not None)
         self.desc = NormDesc(ABI_VERSION, hidden, _mq_dtype(residual_dtype), _mq_dtype(weight_dtype), eps,
                              weight_offset, scale, _ptr(post_weight), _ptr(pre_weight))
         self._ref = ctypes.byref(self.desc)
@@ -490,11 +489,11 @@ class ResidualNorm:
         float32 or bfloat16: [H] per channel, [T, 1] per token or [T, H].
         Returns (residual_out, norm_out); norm_out is None without a
         ``pre_weight``.  The outputs may be the inputs' own buffers."""
-        q = self._q
-        first = x if x is not None else residual
-        if first is None or first.dim() != 2:
+        q, first = self._q, residual if x is None else x
+        given = None if first is None else first.shape
+        if given is None or len(given) != 2:
             raise ValueError("need x or residual [T, H]")
-        t, h, index = len(first), self.hidden, first.get_device()
+        t, h, index = given[0], self.hidden, first.get_device()
         if index >= 0 and index != q.device_now():
             with q.on(index):
                 return self.forward(x, residual, gate, residual_out, norm_out, stream)
@@ -513,10 +512,15 @@ class ResidualNorm:
                 raise ValueError("norm_out needs a pre_weight")
         elif norm_out is None:
             norm_out = _empty(shape, bf16, first.device, stream)
-        if not (index >= 0 and (x is None or _fits(x, shape, bf16, index))
-                and (residual is None or _fits(residual, shape, rd, index)) and _fits(residual_out, shape, rd, index)
-                and (norm_out is None or _fits(norm_out, shape, bf16, index)) and self._index <= {index}
-                and (gate is None or gate.dtype in self._types and _fits(gate, gs, gate.dtype, index))):
+        if not (index >= 0 and self._index <= {index}
+                and (x is None or x.dtype is bf16 and x.shape == shape and x.is_contiguous() and x.get_device() == index)
+                and (residual is None or residual.dtype is rd and residual.shape == shape and residual.is_contiguous()
+                     and residual.get_device() == index)
+                and residual_out.dtype is rd and residual_out.shape == shape and residual_out.is_contiguous()
+                and residual_out.get_device() == index
+                and (norm_out is None or norm_out.dtype is bf16 and norm_out.shape == shape and norm_out.is_contiguous()
+                     and norm_out.get_device() == index)
+                and (gate is None or gate.dtype in self._types and gate.is_contiguous() and gate.get_device() == index)):
             if x is not None:
                 _need(x, "x", shape, (bf16,))
             if residual is not None:
@@ -660,7 +664,7 @@ class Layer:
             raise ValueError("logits_out needs router_w")
         if hidden.dim() != 2:
             raise ValueError("hidden must be [T, H]")
-        index, t, bf16 = hidden.get_device(), len(hidden), q.bf16
+        index, t, bf16 = hidden.get_device(), hidden.shape[0], q.bf16
         if index >= 0 and index != q.device_now():
             with q.on(index):
                 return self.forward_gated(gate, hidden, logits, router_w, residual, out, workspace, activations,

@@ -68,9 +68,11 @@ __device__ __forceinline__ float slot_score(const GateArgs &g, float l, float to
     s *= __builtin_amdgcn_rcpf(z);
   return l > -kInf ? s : 0.f;
 }
-// Divides by a row's sum (0 where every slot is masked).
+// Divides by a row's sum (0 where every slot is masked); the remainder of the
+// first quotient corrects it, so one weight alone is 1.
 __device__ __forceinline__ float over_sum(float s, float sum) {
-  return sum > 0.f ? s * __builtin_amdgcn_rcpf(sum) : 0.f;
+  const float r = __builtin_amdgcn_rcpf(sum), q = s * r;
+  return sum > 0.f ? fmaf(fmaf(-q, sum, s), r, q) : 0.f;
 }
 
 // The exponent of the power of two that brings a token's largest weight m into
