@@ -7,6 +7,14 @@
 // rounding, so the selection is defined on 64-bit scores; the fast gate selects
 // on 32-bit ones, bounds their error and looks again, in 64 bits, where the
 // order lies within it.
+//
+// Measured (sigmoid, bias, k 8, 32-bit logits): 65536 tokens of 128 experts 18.3
+// us (2.1 TB/s), 16384 of 256 in 8 groups, 4 kept, 11.5 us (1.5 TB/s); all in 64
+// bits, a wave a token, 69 and 38 us.  Bound by vector instructions: 501 a wave
+// of four tokens of 128 experts, issued in 75% of the kernel's cycles (880 of 256
+// with groups); the 64-bit second looks take 0.9 us of the 18.3, 1.0 of the 11.5.
+// Loops over several groups of four tokens a wave were slower (26 against 19
+// us: more registers).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

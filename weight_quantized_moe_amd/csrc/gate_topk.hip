@@ -19,7 +19,10 @@ __global__ __launch_bounds__(256) void gate_topk_kernel(GateArgs g, const void *
 hipError_t launch_gate_topk(const GateArgs &g, const void *logits, int bf16, int64_t T, const GateOut &o,
                             hipStream_t s) {
   return with_gate_variant<true>(g, [&](auto per, auto mode) {
-    // one wave a workgroup spreads a small batch over the CUs
+    // One wave a workgroup spreads a small batch over the CUs (3001 tokens of 72
+    // experts: 6.0 us, two waves 6.3); a large one is bound by the rate at which
+    // workgroups start with it (65536 of 128: 29 us; 2, 4, 8 and 16 waves 21.8,
+    // 19.7, 20.6 and 22.4; 16384 of 256: 16.3, then 13.0, 12.7, 13.0 and 12.7).
     const int threads = T <= 4096 ? 64 : 256, tpb = threads / 16;
     hipLaunchKernelGGL((gate_topk_kernel<per(), mode()>), dim3((unsigned)((T + tpb - 1) / tpb)), dim3(threads), 0, s, g,
                        logits, bf16, T, o);

@@ -10,6 +10,12 @@
 // consecutive over the lanes.  Rows whose length is no multiple of 8 start at
 // odd addresses: the same accesses, which the hardware takes at any alignment of
 // the element (see Ends for the row's last lane).
+//
+// Measured: 16384 rows of 2048, both norms, BF16: 50 us (5.4 TB/s, a plain copy
+// of that size 5.5); 4096 rows of 8192 with a 32-bit residual 63-67 us (5.0-5.3
+// TB/s); 16384 odd rows of 1023 with a 32-bit residual and a full gate 52 us
+// (4.5), of 1024 45 us.  With the row in LDS and one value a lane: 158 and 234
+// us for the first two.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -264,6 +270,10 @@ static void norm_launch(const NormArgs &a, int64_t T, int threads, hipStream_t s
   hipLaunchKernelGGL(f, dim3((unsigned)((T + kRows - 1) / kRows)), dim3(threads), 0, s, a, T);
 }
 
+// Few values a lane and many lanes a row: with 8 a lane everything a row needs is
+// in flight at once (16384 rows of 2048: 51 us; 16 a lane 54, 32 a lane, one wave a
+// row, 60).  Rows of up to 512 share a workgroup, of up to 256 a wave (50000 rows
+// of 128: 25.7 -> 17.0 us).
 hipError_t launch_norm(const NormArgs &a, int64_t T, hipStream_t s) {
   const int eights = (a.H + 7) / 8;
   if (eights <= 16)
