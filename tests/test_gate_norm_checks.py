@@ -3,6 +3,8 @@ GPU: every call here is refused or has no tokens)."""
 import ctypes
 import math
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,7 +13,7 @@ import torch
 from oracle import gate as ogate
 from oracle import moe as omoe
 from oracle import norm as onorm
-from weight_quantized_moe_amd import Gate, Layer, MoeQuantError, ResidualNorm, binding
+from weight_quantized_moe_amd import Gate, Layer, MoeQuantError, ResidualNorm, binding, build
 from weight_quantized_moe_amd.binding import GateDesc, LayerDesc, NormDesc
 
 OK, NULL, SHAPE, ALIGN, FORMAT, DTYPE, WORKSPACE, ABI = range(8)
@@ -23,6 +25,26 @@ def lib():
     if not os.path.exists(binding.library_path()):
         pytest.fail("libmoe_quant.so is not built (run __graft_entry__.build())")
     return binding.load_library()
+
+
+@pytest.mark.timeout(900)
+def test_checks_under_address_sanitizer():
+    """This file again, with AddressSanitizer on the library's host code."""
+    if os.environ.get("MOE_QUANT_LIB"):
+        pytest.skip("runs on another library already")
+    from test_abi_asan import _stale
+    try:
+        runtime = build.asan_runtime()
+    except RuntimeError as e:
+        pytest.skip(str(e))
+    if _stale(build.ASAN_LIB):
+        build.build_asan()
+    env = dict(os.environ, MOE_QUANT_LIB=build.ASAN_LIB, LD_PRELOAD=runtime,
+               ASAN_OPTIONS="detect_leaks=0:abort_on_error=1")
+    res = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", os.path.abspath(__file__)],
+                         env=env, capture_output=True, text=True, timeout=600)
+    tail = (res.stdout + res.stderr)[-3000:]
+    assert res.returncode == 0 and "AddressSanitizer" not in res.stderr, tail
 
 
 def test_struct_layouts_match_header():

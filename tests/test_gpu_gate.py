@@ -12,6 +12,12 @@ from weight_quantized_moe_amd import Gate
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
 def as_f64(logits):
     return logits.float().cpu().numpy().astype(np.float64)
 

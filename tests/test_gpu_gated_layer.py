@@ -8,10 +8,18 @@ import torch
 from oracle import gate as ogate
 from oracle import moe as omoe
 from oracle import norm as onorm
-from tests.gpu_helpers import ATOL_MAX, RTOL_L2, GpuLayer, dev, random_layer
+from gpu_helpers import ATOL_MAX, RTOL_L2, GpuLayer, random_layer
 from weight_quantized_moe_amd import Gate, MoeQuantError, ResidualNorm, router_logits
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
 FORMATS = ["int4_g128", "fp8_b128", "nvfp4_g16"]
 BF = torch.bfloat16
 
@@ -258,3 +266,66 @@ def test_a_block_as_it_is_used(t):
     assert np.allclose(f64(stream2), r + add, rtol=0, atol=2e-5 * np.abs(r + add).max())
     ref = onorm.rms_norm(f64(stream2), f64(norms[2]), 1e-6, 0.0)
     assert np.all(np.abs(f64(nxt) - ref) <= (2.0 ** -8 + 1e-5) * np.abs(ref))
+
+
+@pytest.mark.parametrize("t", [1, 16, 17, 300])
+def test_a_block_in_a_graph(t):
+    """The whole block captured, and replayed on other inputs between eager runs
+    of it on buffers of their own."""
+    e, k, h, i = 16, 4, 256, 128
+    lay = GpuLayer(*random_layer("nvfp4_g16", 11, e, h, i), k)
+    d = make(t, e, h, seed=t)
+    router = (0.1 * torch.randn(e, h, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))).to(BF)
+    w = torch.ones(h, device="cuda")
+    before = ResidualNorm(h, pre_weight=w, residual_dtype=torch.float32)
+    after = ResidualNorm(h, post_weight=w, pre_weight=w, residual_dtype=torch.float32, scale=0.5)
+    gate = gate_of(e, k, d["bias"], **GROUPED)
+
+    def block(x, stream):
+        s1, n = before.forward(x, stream)
+        y = lay.layer.forward_gated(gate, n, router_w=router)
+        return after.forward(y, s1)
+
+    x, stream = d["x"].clone(), d["r"].float()
+    warm = torch.cuda.Stream()
+    with torch.cuda.stream(warm):
+        block(x, stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, nxt = block(x, stream)
+    for r in range(3):
+        x.copy_(make(t, e, h, seed=70 + r)["x"])
+        graph.replay()
+        eager_out, eager_nxt = block(x, stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager_out) and torch.equal(nxt, eager_nxt)
+
+
+def test_two_threads():
+    """Host threads with streams and workspaces of their own on one layer and gate."""
+    import threading
+    lay = GpuLayer(*random_layer("int4_g128", 7, 16, 256, 128), 4)
+    gate = Gate(16, 4, score="sigmoid")
+    cases = [make(t, 16, 256, seed=t) for t in (5, 40)]
+    ref = [lay.layer.forward_gated(gate, d["x"], logits=d["lg"]) for d in cases]
+    ids = [gate.topk(d["lg"])[0] for d in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(n):
+        d, s = cases[n], torch.cuda.Stream()
+        ws = lay.layer.workspace(d["x"].shape[0])
+        for _ in range(50):
+            out = lay.layer.forward_gated(gate, d["x"], logits=d["lg"], workspace=ws, stream=s)
+            got, _ = gate.topk(d["lg"], stream=s)
+            s.synchronize()
+            if not (torch.equal(out, ref[n]) and torch.equal(got, ids[n])):
+                wrong.append(n)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in (0, 1)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong

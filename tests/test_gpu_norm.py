@@ -7,6 +7,14 @@ from oracle import norm as onorm
 from weight_quantized_moe_amd import ResidualNorm
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
 BF, F32 = torch.bfloat16, torch.float32
 
 
