@@ -50,8 +50,8 @@ __global__ __launch_bounds__(256) void gate_stage_kernel(GateArgs g, const void 
 // and grouping in one workgroup (route_group_kernel's counterpart): waves 0 to 3
 // take the gate of 4 tokens each, waves 4 to 7 their rows' powers of two, and
 // all of them the grouping on the ids and weights in LDS.  One token of 128
-// experts: 6.0 us, bound by the latency of its steps; in three launches the
-// layer's step took 23.2 us, with this one 18.6.
+// experts: 5.6 us, bound by the latency of its steps; in three launches the
+// layer's step took 23.2 us, with this one 18.6, and with group_few 18.2.
 // ---------------------------------------------------------------------------
 struct GroupArgs {
   int32_t *offsets, *mtile;
@@ -60,6 +60,57 @@ struct GroupArgs {
   int4 *rowinfo;
   int32_t *inv_pos, *p_offsets, *p_sorted_tok, *p_inv;
 };
+// Grouping of R = T k <= 64 slots (T <= kFusedT) without a barrier: lane i is slot
+// i in every wave, and a slot's row is the number of slots before it in the order
+// (expert, slot), counted over the slots.  No expert has more than kFusedT rows:
+// one 16-row chunk and one M-tile each.
+static_assert(kFusedT <= 16 && kFusedT <= kPrefillBM, "one chunk and one M-tile an expert");
+__device__ __forceinline__ void group_few(const int32_t *ids, const float *wts, const float *rowscale, int T, int E,
+                                          int k, const GroupArgs &q) {
+  const int tid = threadIdx.x, lane = tid & 63, R = T * k;
+  const int e = lane < R ? ids[lane] : kMaxExperts;
+  int below = 0, same = 0, earlier = 0;  // slots of lower experts, of this one, of this one before this slot
+  for (int j = 0; j < R; ++j) {
+    const int ej = __builtin_amdgcn_readlane(e, j);
+    below += ej < e;
+    same += ej == e;
+    earlier += ej == e && j < lane;
+  }
+  const uint64_t firsts = __ballot(lane < R && earlier == 0);
+  const int active = __popcll(firsts);
+  for (int x = tid; x <= E; x += 512) {
+    int rows = 0, experts = 0;
+    for (int j = 0; j < R; ++j) {
+      const bool lower = __builtin_amdgcn_readlane(e, j) < x;
+      rows += lower;
+      experts += lower && ((firsts >> j) & 1ull);
+    }
+    q.offsets[x] = rows;
+    if (q.p_offsets) q.p_offsets[x] = rows;
+    q.mtile[x] = experts;
+  }
+  if (tid >= 64) return;
+  int rank = 0;  // active experts below this one
+  for (int j = 0; j < R; ++j) rank += __builtin_amdgcn_readlane(e, j) < e && ((firsts >> j) & 1ull);
+  if (lane < R) {
+    const int pos = below + earlier, t = lane / k;
+    q.sorted_slots[pos] = lane;
+    q.rowinfo[pos] = int4{lane, t, __builtin_bit_cast(int, rowscale ? rowscale[t] : 0.f),
+                          __builtin_bit_cast(int, wts[lane])};
+    q.inv_pos[lane] = pos;
+    if (q.p_sorted_tok) q.p_sorted_tok[pos] = t;
+    if (q.p_inv) q.p_inv[lane] = pos;
+    if (earlier == 0) {
+      q.einfo[1 + rank] = int4{e, below, same, 0};
+      q.rcp[rank] = rank;
+    }
+  }
+  if (lane == 0) {
+    q.einfo[0] = int4{active, active, 0, 0};
+    q.rcp[active] = active;
+  }
+}
+
 template <int kPer, GateMode kMode>
 __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                          GateOut o, StageArgs a, GroupArgs q) {
@@ -92,6 +143,10 @@ __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void 
   }
   const bool scales = a.stage_rows == 2;
   if (scales && (int)threadIdx.x < a.T) a.rowscale[threadIdx.x] = s_rs[threadIdx.x];
+  if (a.T * g.k <= 64) {
+    group_few(s_ids, s_wts, scales ? s_rs : nullptr, a.T, g.E, g.k, q);
+    return;
+  }
   group_small_body<512>(s_ids, s_wts, scales ? s_rs : nullptr, a.T, g.E, g.k, q.offsets, q.mtile, q.einfo, q.rcp,
                         q.sorted_slots, q.rowinfo, q.inv_pos, q.p_offsets, q.p_sorted_tok, q.p_inv, s_ids);
 }
