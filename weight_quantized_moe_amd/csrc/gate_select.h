@@ -241,8 +241,8 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
 // for a sigmoid (exponent 2^-23 |l| s(1 - s) <= 2^-25, reciprocal and sums), and
 // for a softmax by 2^-22 + 2^-24 |c| and a common factor 1 + 2^-18 (its sum: at
 // most 35 additions, 32 experts a lane, and the terms' own errors), so two
-// scores further apart than tol = 2^-19 (1 + |c|), for a softmax 2^-17 (1 +
-// |c|), are in their order.  tau is lowered by tol.  Where two candidates next
+// scores further apart than tol = 2^-20 (1 + |c|), for a softmax 2^-17 (1 +
+// |c|), are in their order with a factor of 2 to spare.  tau is lowered by tol.  Where two candidates next
 // to each other in the order are within tol and not the same logit and bias,
 // the row's candidates are ranked again by 64-bit scores; where a kept and a
 // dropped group are within 2 tol, the groups are, by the 64-bit scores of each
@@ -401,7 +401,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   const bool softmax = kFixed && !kByLogit ? kMode == kSoftmax || kMode == kSoftmaxGroups
                                            : g.score == MQ_SCORE_SOFTMAX;
   const bool sums = groups && g.group_top == 2;
-  const float tol1 = softmax ? 0x1p-17f : 0x1p-19f;
+  const float tol1 = softmax ? 0x1p-17f : 0x1p-20f;
   // without whole lanes: what a lane loads beyond its experts is some other
   // logit, and its key is 0; only the array's end must not be passed
   const int64_t left = (T - t0) * g.E;  // logits from the wave's first on
@@ -562,9 +562,9 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
         unsure = close && n > 2;
       }
     }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = kept ? key[i] : 0u;
   }
+  // a lane of a dropped group has no keys from here on
+  const uint32_t drop = kept ? 0u : 0xFFFFFFFFu;
   t1 = kept ? t1 : 0u;
   t2 = kept ? t2 : 0u;
   // the least of the k largest of the lanes' two largest
@@ -588,6 +588,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
     return by_logit || k0 <= kMaskedKey ? k0 : score_key((v - tol1 * (1.f + fabsf(v))) + 0.f);
   };
   auto at_least = [&](uint32_t k0) {  // keys of this lane
+    k0 |= drop;
     int c = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) c += key[i] >= k0;
@@ -602,7 +603,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       uint32_t up = 0xFFFFFFFFu;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) up = min(up, key[i] > tau ? key[i] : 0xFFFFFFFFu);
-      up = min16_u32(up);
+      up = min16_u32(up | drop);
       more &= sum16i(at_least(up)) >= g.k;
       tau = more ? up : tau;
       lo = least(tau);
@@ -627,7 +628,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       int pa = before, pe = all + pos0 - before;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (fits && key[i] >= tau) {
+        if (fits && key[i] >= (tau | drop)) {
           const int p = key[i] > tau ? pa++ : pe++;
           if (p < kFastK) {
             cd.key[p] = key[i];
@@ -642,7 +643,7 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   int pos = pos0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (key[i] >= lo) {
+    if (key[i] >= (lo | drop)) {
       cd.key[pos] = key[i];
       cd.l[pos] = l[i];
       cd.id[pos] = a.e0 + i;
