@@ -376,11 +376,11 @@ __device__ __forceinline__ GateLane gate_lane(const GateArgs &g, int li) {
   return a;
 }
 
-// What of a gate is fixed when a kernel is compiled.  kAny: nothing; kFull: each
-// lane holds kPer experts (E = 16 kPer), loaded 16 bytes at a time; the others:
-// that, the source of the order (logits, sigmoid or softmax plus bias), and
-// whether there are groups.  Branches on these took a fifth of the kernel.
-enum GateMode { kAny, kFull, kLogits, kSigmoid, kSoftmax, kLogitsGroups, kSigmoidGroups, kSoftmaxGroups };
+// What of a gate is fixed when a kernel is compiled.  kAny: nothing; the others:
+// each lane holds kPer experts (E = 16 kPer), loaded 16 bytes at a time, the
+// source of the order (logits, sigmoid or softmax plus bias), and whether there
+// are groups.  Branches on these took a tenth of the kernel's time.
+enum GateMode { kAny, kLogits, kSigmoid, kSoftmax, kLogitsGroups, kSigmoidGroups, kSoftmaxGroups };
 
 template <int kPer, GateMode kMode>
 __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *__restrict__ logits, int bf16,
@@ -393,12 +393,12 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   const bool here = row < rows;
   const int r = min(row, rows - 1);  // a row past the last token repeats it
   const uint32_t t = (uint32_t)t0 + r;
-  constexpr bool kWhole = kMode != kAny, kFixed = kMode > kFull;
+  constexpr bool kWhole = kMode != kAny;
   constexpr bool kByLogit = kMode == kLogits || kMode == kLogitsGroups;
   constexpr bool kGroups = kMode >= kLogitsGroups;
   const GateLane a = gate_lane<kPer, kWhole>(g, li);
-  const bool by_logit = kFixed ? kByLogit : g.bias == nullptr, groups = kFixed ? kGroups : g.groups > 1;
-  const bool softmax = kFixed && !kByLogit ? kMode == kSoftmax || kMode == kSoftmaxGroups
+  const bool by_logit = kWhole ? kByLogit : g.bias == nullptr, groups = kWhole ? kGroups : g.groups > 1;
+  const bool softmax = kWhole && !kByLogit ? kMode == kSoftmax || kMode == kSoftmaxGroups
                                            : g.score == MQ_SCORE_SOFTMAX;
   const bool sums = groups && g.group_top == 2;
   const float tol1 = softmax ? 0x1p-17f : 0x1p-20f;
@@ -734,8 +734,7 @@ __device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restr
 }
 
 // Calls f with the kernel variant for this gate: f(kPer, mode) as constants.
-// kFixed: with the modes beyond kFull.
-template <bool kFixed, typename F>
+template <typename F>
 static hipError_t with_gate_variant(const GateArgs &g, F f) {
   using std::integral_constant;
   const int lanes = 16 / g.groups;  // 0 above 16 groups
@@ -745,18 +744,12 @@ static hipError_t with_gate_variant(const GateArgs &g, F f) {
   const bool full = chunk * 16 == g.E;
   auto go = [&](auto n) {
     if (!full || chunk != n()) return f(n, integral_constant<GateMode, kAny>{});
-    if constexpr (kFixed) {
-      const bool groups = g.groups > 1;
-      if (!g.bias)
-        return groups ? f(n, integral_constant<GateMode, kLogitsGroups>{}) : f(n, integral_constant<GateMode, kLogits>{});
-      if (g.score == MQ_SCORE_SIGMOID)
-        return groups ? f(n, integral_constant<GateMode, kSigmoidGroups>{})
-                      : f(n, integral_constant<GateMode, kSigmoid>{});
-      return groups ? f(n, integral_constant<GateMode, kSoftmaxGroups>{})
-                    : f(n, integral_constant<GateMode, kSoftmax>{});
-    } else {
-      return f(n, integral_constant<GateMode, kFull>{});
-    }
+    const bool groups = g.groups > 1;
+    if (!g.bias)
+      return groups ? f(n, integral_constant<GateMode, kLogitsGroups>{}) : f(n, integral_constant<GateMode, kLogits>{});
+    if (g.score == MQ_SCORE_SIGMOID)
+      return groups ? f(n, integral_constant<GateMode, kSigmoidGroups>{}) : f(n, integral_constant<GateMode, kSigmoid>{});
+    return groups ? f(n, integral_constant<GateMode, kSoftmaxGroups>{}) : f(n, integral_constant<GateMode, kSoftmax>{});
   };
   if (chunk <= 4) return go(integral_constant<int, 4>{});
   if (chunk <= 8) return go(integral_constant<int, 8>{});

@@ -18,7 +18,7 @@ __global__ __launch_bounds__(256) void gate_topk_kernel(GateArgs g, const void *
 
 hipError_t launch_gate_topk(const GateArgs &g, const void *logits, int bf16, int64_t T, const GateOut &o,
                             hipStream_t s) {
-  return with_gate_variant<true>(g, [&](auto per, auto mode) {
+  return with_gate_variant(g, [&](auto per, auto mode) {
     // One wave a workgroup spreads a small batch over the CUs (3001 tokens of 72
     // experts: 6.0 us, two waves 6.3); a large one is bound by the rate at which
     // workgroups start with it (65536 of 128: 29 us; 2, 4, 8 and 16 waves 21.8,
