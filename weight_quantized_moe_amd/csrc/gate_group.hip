@@ -67,7 +67,7 @@ __device__ __forceinline__ void group_few(const int32_t *ids, const float *wts, 
   }
 }
 
-template <int kPer, GateMode kMode>
+template <int kPer, GateMode kMode, bool kWhole>
 __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                          GateOut o, StageArgs a, GroupArgs q) {
   __shared__ GateLds lds[4];
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void 
   if (t0 < a.T) {
     if (wave < 4) {
       const GateOut in_lds = {s_ids, s_wts, o.wscale, o.p_ids, o.p_w};
-      gate_wave<kPer, kMode>(g, logits, bf16, t0, a.T, lane, &lds[wave], in_lds);
+      gate_wave<kPer, kMode, kWhole>(g, logits, bf16, t0, a.T, lane, &lds[wave], in_lds);
     } else if (a.stage_rows == 2) {
       u4 v[4][4];
 #pragma unroll
@@ -109,8 +109,8 @@ __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void 
 
 hipError_t launch_gate_group(const GateArgs &g, const void *logits, int bf16, const GateOut &o, const StageArgs &a,
                              const GroupArgs &q, hipStream_t s) {
-  return with_gate_variant(g, [&](auto per, auto mode) {
-    hipLaunchKernelGGL((gate_group_kernel<per(), mode()>), dim3(1), dim3(512), 0, s, g, logits, bf16, o, a, q);
+  return with_gate_variant(g, [&](auto per, auto mode, auto whole) {
+    hipLaunchKernelGGL((gate_group_kernel<per(), mode(), whole()>), dim3(1), dim3(512), 0, s, g, logits, bf16, o, a, q);
     return hipGetLastError();
   });
 }

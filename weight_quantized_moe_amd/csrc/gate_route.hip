@@ -17,7 +17,7 @@ namespace mq {
 // 10.6 us (32 MB of rows: 3.2 TB/s), the layer 429 -> 417 us; 61 tokens 5.4 us,
 // the layer 113 -> 106 us.
 // ---------------------------------------------------------------------------
-template <int kPer, GateMode kMode>
+template <int kPer, GateMode kMode, bool kWhole>
 __global__ __launch_bounds__(256) void gate_stage_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                          GateOut o, StageArgs a) {
   __shared__ GateLds lds[4];
@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void gate_stage_kernel(GateArgs g, const void 
   if (blockIdx.x == 0 && threadIdx.x == 0) a.flags[0] = 0u;
   if ((int)blockIdx.x < a.gate_blocks) {
     const int64_t t0 = ((int64_t)blockIdx.x * waves + wave) * 4;
-    if (t0 < a.T) gate_wave<kPer, kMode>(g, logits, bf16, t0, a.T, lane, &lds[wave], o);
+    if (t0 < a.T) gate_wave<kPer, kMode, kWhole>(g, logits, bf16, t0, a.T, lane, &lds[wave], o);
     return;
   }
   const int t0 = (((int)blockIdx.x - a.gate_blocks) * waves + wave) * 4, T = a.T, H = a.H;
@@ -61,11 +61,11 @@ hipError_t launch_route_gated(const LayerDims &L, const FwdPtrs &P, const Worksp
                          (int32_t *)(ws + W.inv_pos), P.p_offsets, P.p_sorted_tok, P.p_inv};
     return launch_gate_group(*P.gated, logits, bf16, o, a, q, s);
   }
-  return with_gate_variant(*P.gated, [&](auto per, auto mode) {
+  return with_gate_variant(*P.gated, [&](auto per, auto mode, auto whole) {
     const int threads = P.T <= 4096 ? 64 : 256, tpb = threads / 16;
     a.gate_blocks = (P.T + tpb - 1) / tpb;
     const unsigned blocks = (unsigned)a.gate_blocks * (stage_rows ? 2u : 1u);
-    hipLaunchKernelGGL((gate_stage_kernel<per(), mode()>), dim3(blocks), dim3(threads), 0, s, *P.gated, logits, bf16, o, a);
+    hipLaunchKernelGGL((gate_stage_kernel<per(), mode(), whole()>), dim3(blocks), dim3(threads), 0, s, *P.gated, logits, bf16, o, a);
     return hipGetLastError();
   });
 }

@@ -376,13 +376,13 @@ __device__ __forceinline__ GateLane gate_lane(const GateArgs &g, int li) {
   return a;
 }
 
-// What of a gate is fixed when a kernel is compiled.  kAny: nothing; the others:
-// each lane holds kPer experts (E = 16 kPer), loaded 16 bytes at a time, the
-// source of the order (logits, sigmoid or softmax plus bias), and whether there
-// are groups.  Branches on these took a tenth of the kernel's time.
-enum GateMode { kAny, kLogits, kSigmoid, kSoftmax, kLogitsGroups, kSigmoidGroups, kSoftmaxGroups };
+// What of a gate is fixed when a kernel is compiled: the source of the order
+// (logits, sigmoid or softmax plus bias) and whether there are groups.  Branches
+// on these took a tenth of the kernel's time.  kWhole beside it: each lane holds
+// kPer experts (E = 16 kPer), loaded 16 bytes at a time.
+enum GateMode { kLogits, kSigmoid, kSoftmax, kLogitsGroups, kSigmoidGroups, kSoftmaxGroups };
 
-template <int kPer, GateMode kMode>
+template <int kPer, GateMode kMode, bool kWhole>
 __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *__restrict__ logits, int bf16,
                                                  int64_t t0, int64_t T, int lane, Candidates *cands,
                                                  const GateOut &o) {
@@ -393,13 +393,11 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   const bool here = row < rows;
   const int r = min(row, rows - 1);  // a row past the last token repeats it
   const uint32_t t = (uint32_t)t0 + r;
-  constexpr bool kWhole = kMode != kAny;
   constexpr bool kByLogit = kMode == kLogits || kMode == kLogitsGroups;
   constexpr bool kGroups = kMode >= kLogitsGroups;
   const GateLane a = gate_lane<kPer, kWhole>(g, li);
-  const bool by_logit = kWhole ? kByLogit : g.bias == nullptr, groups = kWhole ? kGroups : g.groups > 1;
-  const bool softmax = kWhole && !kByLogit ? kMode == kSoftmax || kMode == kSoftmaxGroups
-                                           : g.score == MQ_SCORE_SOFTMAX;
+  constexpr bool by_logit = kByLogit, groups = kGroups;
+  const bool softmax = by_logit ? g.score == MQ_SCORE_SOFTMAX : kMode == kSoftmax || kMode == kSoftmaxGroups;
   const bool sums = groups && g.group_top == 2;
   const float tol1 = softmax ? 0x1p-17f : 0x1p-20f;
   // without whole lanes: what a lane loads beyond its experts is some other
@@ -722,34 +720,38 @@ union GateLds {
   Candidates cand[4];
   double sc[kMaxExperts];
 };
-template <int kPer, GateMode kMode>
+template <int kPer, GateMode kMode, bool kWhole>
 __device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restrict__ logits, int bf16, int64_t t0,
                                           int64_t T, int lane, GateLds *lds, const GateOut &o) {
   t0 = __builtin_amdgcn_readfirstlane((int)t0);  // the same in every lane: kept in scalar registers
   uint32_t redo = 0xFu;
-  if constexpr (kPer > 0) redo = gate_tokens4<kPer, kMode>(g, logits, bf16, t0, T, lane, lds->cand, o);
+  if constexpr (kPer > 0) redo = gate_tokens4<kPer, kMode, kWhole>(g, logits, bf16, t0, T, lane, lds->cand, o);
   constexpr int kPer64 = kPer == 0 ? kMaxExperts / 64 : kPer <= 4 ? 1 : kPer / 4;
   for (int r = 0; r < 4 && t0 + r < T; ++r)
     if ((redo >> r) & 1u) gate_token<kPer64>(g, logits, bf16, t0 + r, lane, lds->sc, o);
 }
 
-// Calls f with the kernel variant for this gate: f(kPer, mode) as constants.
+// Calls f with the kernel variant for this gate: f(kPer, mode, kWhole) as constants.
 template <typename F>
 static hipError_t with_gate_variant(const GateArgs &g, F f) {
   using std::integral_constant;
   const int lanes = 16 / g.groups;  // 0 above 16 groups
   if (g.k > kFastK || lanes == 0 || 16 % g.groups)
-    return f(integral_constant<int, 0>{}, integral_constant<GateMode, kAny>{});
+    return f(integral_constant<int, 0>{}, integral_constant<GateMode, kLogits>{}, std::false_type{});
   const int chunk = (g.per + lanes - 1) / lanes;
-  const bool full = chunk * 16 == g.E;
+  auto whole = [&](auto n, auto mode) {
+    return chunk * 16 == g.E && chunk == n() ? f(n, mode, std::true_type{}) : f(n, mode, std::false_type{});
+  };
   auto go = [&](auto n) {
-    if (!full || chunk != n()) return f(n, integral_constant<GateMode, kAny>{});
     const bool groups = g.groups > 1;
     if (!g.bias)
-      return groups ? f(n, integral_constant<GateMode, kLogitsGroups>{}) : f(n, integral_constant<GateMode, kLogits>{});
+      return groups ? whole(n, integral_constant<GateMode, kLogitsGroups>{})
+                    : whole(n, integral_constant<GateMode, kLogits>{});
     if (g.score == MQ_SCORE_SIGMOID)
-      return groups ? f(n, integral_constant<GateMode, kSigmoidGroups>{}) : f(n, integral_constant<GateMode, kSigmoid>{});
-    return groups ? f(n, integral_constant<GateMode, kSoftmaxGroups>{}) : f(n, integral_constant<GateMode, kSoftmax>{});
+      return groups ? whole(n, integral_constant<GateMode, kSigmoidGroups>{})
+                    : whole(n, integral_constant<GateMode, kSigmoid>{});
+    return groups ? whole(n, integral_constant<GateMode, kSoftmaxGroups>{})
+                  : whole(n, integral_constant<GateMode, kSoftmax>{});
   };
   if (chunk <= 4) return go(integral_constant<int, 4>{});
   if (chunk <= 8) return go(integral_constant<int, 8>{});
