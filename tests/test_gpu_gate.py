@@ -214,6 +214,23 @@ def test_groups_closer_than_a_32_bit_rounding(score):
                   groups=groups, topk_groups=3, group_top=top_n)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (4, 1), (8, 3), (3, 2)])
+def test_biases_whose_sums_pass_32_bits(score, groups, topk_groups):
+    # the type's lowest value is a number, not a mask: a group that holds nothing
+    # else comes before one that is masked, a group of larger numbers before both
+    e, k = 96, 6
+    per, low = e // groups, torch.finfo(torch.float32).min
+    for values in ((-math.inf, low, 0.75 * low), (low, -math.inf, low), (0.75, 1.0, 0.875), (0.0, low, math.inf)):
+        size = 1.0 if abs(values[0]) > 1.0 or values[0] == 0.0 else -low
+        bias = torch.empty(e, device="cuda")
+        for i in range(groups):
+            bias[i * per:(i + 1) * per] = values[min(i, 2)] * size
+        bias[per // 2] = 0.5 * low
+        check(logits(9, e, seed=groups), k, bias=bias, score=score, groups=groups, topk_groups=topk_groups,
+              group_top=2 if groups > 1 else 1)
+
+
 def test_many_tokens_and_limits():
     check(logits(5000, 64, seed=9), 4, bias=a_bias(64), score="sigmoid", groups=8, topk_groups=4, group_top=2, scale=2.5)
     g = Gate(16, 2)

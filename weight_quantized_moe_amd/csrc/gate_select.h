@@ -8,13 +8,13 @@
 // on 32-bit ones, bounds their error and looks again, in 64 bits, where the
 // order lies within it.
 //
-// Measured (sigmoid, bias, k 8, 32-bit logits): 65536 tokens of 128 experts 18.3
-// us (2.1 TB/s), 16384 of 256 in 8 groups, 4 kept, 11.5 us (1.5 TB/s); all in 64
+// Measured (sigmoid, bias, k 8, 32-bit logits): 65536 tokens of 128 experts 18.0
+// us (2.1 TB/s), 16384 of 256 in 8 groups, 4 kept, 11.4 us (1.6 TB/s); all in 64
 // bits, a wave a token, 69 and 38 us.  Bound by vector instructions: 501 a wave
-// of four tokens of 128 experts, issued in 75% of the kernel's cycles (880 of 256
-// with groups); the 64-bit second looks take 0.9 us of the 18.3, 1.0 of the 11.5.
-// Loops over several groups of four tokens a wave were slower (26 against 19
-// us: more registers).
+// of four tokens of 128 experts, issued in 75% of the kernel's cycles (867 of 256
+// with groups); finding close scores and the 64-bit second looks take 1.9 us of
+// the 18.0, 1.4 of the 11.4.  Loops over several groups of four tokens a wave
+// were slower (26 against 19 us: more registers).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -245,7 +245,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
 // |c|), are in their order with a factor of 2 to spare.  tau is lowered by tol.  Where two candidates next
 // to each other in the order are within tol and not the same logit and bias,
 // the row's candidates are ranked again by 64-bit scores; where a kept and a
-// dropped group are within 2 tol, the groups are, by the 64-bit scores of each
+// dropped group are within 2 tol (their sums of two, too: those add two errors), the groups are, by the 64-bit scores of each
 // lane's two largest.  Without a bias the keys are the logits and exact, and
 // masked experts (key of -inf) are exact always: of more than 16 candidates
 // those equal to tau then count in expert order only.  What is left (more than
@@ -518,14 +518,15 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
       }
       size = fmaxf(fabsf(s1), sums ? fabsf(s2) : 0.f);
       size = size < kInf ? size : 0.f;
-      gk = score_key((sums ? s1 + s2 : s1) + 0.f);
+      // half the sum: two of the largest numbers' must not pass for an infinity
+      gk = score_key((sums ? fmaf(0.5f, s1, 0.5f * s2) : s1) + 0.f);
     }
     kept = groups_before<1>(gk, a.lower, a.lanes) < g.topk_groups;
     if ((sums || !by_logit) && g.topk_groups < g.groups) {
       const float lo = from_ordered_key(min16_u32(kept ? gk : 0xFFFFFFFFu));
       const float hi = from_ordered_key(max16_u32(kept ? 0u : gk));
       // -inf on either side is exact (masked experts): the difference is then inf or NaN
-      const bool close = lo - hi <= 2.f * tol1 * (1.f + max16f(size));
+      const bool close = lo - hi <= (sums ? tol1 : 2.f * tol1) * (1.f + max16f(size));
       if (__any(close)) {
         // the 64-bit scores of the lane's two largest, which have to be its two
         // largest for certain
