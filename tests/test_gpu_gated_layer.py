@@ -163,6 +163,26 @@ def test_weights_of_any_size_keep_their_digits(t):
     check(lay, gate_of(16, 4, **kw), kw, far, residual=False)
 
 
+@pytest.mark.parametrize("t", [3, 12, 40])
+def test_saturates_no_earlier_than_the_layers_own_routing(t):
+    """Expert outputs between 131000 and 262000 times weights of a quarter fit FP16.
+    The outputs are linear in the down projection's scales, so a power of two on
+    those sets their size."""
+    p13, p2 = random_layer("fp8_b128", 7, 16, 256, 128)
+    d = make(t, 16, 256, seed=t)
+    d["lg"] = torch.zeros_like(d["lg"])
+    lay = GpuLayer(p13, p2, 4)
+    alone = [oracle_layer(lay, np.full((t, 1), e, np.int32), np.ones((t, 1)), bits(d["x"]))[0] for e in range(4)]
+    p2.scale[:] = p2.scale * 2.0 ** np.floor(np.log2(262000 / np.abs(alone).max()))
+    lay = GpuLayer(p13, p2, 4)
+    ws = lay.layer.workspace(t)
+    a = lay.layer.forward(d["lg"], d["x"], workspace=ws)
+    assert not lay.layer.check(ws)
+    b = lay.layer.forward_gated(Gate(16, 4), d["x"], logits=d["lg"], workspace=ws)
+    assert not lay.layer.check(ws)
+    assert torch.equal(a, b)          # weights of exactly a quarter in both
+
+
 def test_masked_rows():
     """A row without live experts gives the residual, and rows with few take
     their live experts alone."""

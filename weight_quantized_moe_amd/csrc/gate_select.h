@@ -84,9 +84,11 @@ __device__ __forceinline__ float over_sum(float s, float sum) {
 }
 
 // The exponent of the power of two that brings a token's largest weight m into
-// [2^-1, 1).
+// [2^-1, 1); 0 (none) for 2^-7 to 1, where every renormalised row of up to 64
+// slots lies: such a row's products saturate in FP16 no earlier than under the
+// layer's own routing.
 __device__ __forceinline__ int weight_exponent(float m) {
-  if (!(m > 0.f)) return 0;
+  if (!(m > 0.f) || (m >= 0x1p-7f && m <= 1.f)) return 0;
   const int ex = (int)(__builtin_bit_cast(uint32_t, m) >> 23) - 126;
   return ex < -120 ? -120 : ex > 120 ? 120 : ex;
 }

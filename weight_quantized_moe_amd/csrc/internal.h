@@ -159,7 +159,7 @@ struct GateArgs {
   const float *bias;  // [E] or null
 };
 // Where the gate's results go.  wscale (nullable): a power of two per token is
-// taken out of wts, which then lie in [2^-1, 1) at their largest, and written
+// taken out of wts, which then lie in [2^-7, 1] at their largest, and written
 // there (the expert layer rounds its per-slot products to FP16).  p_ids and p_w
 // (nullable): copies with the weights themselves.
 struct GateOut {
