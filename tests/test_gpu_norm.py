@@ -148,6 +148,19 @@ def test_offsets_past_32_bits():
     assert torch.equal(r[-3:], small) and torch.all(r[-4] == 0)
 
 
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("rd", [BF, F32])
+def test_more_rows_than_a_launch_takes(gate, rd):
+    t, h, k = (1 << 21) + 5, 16, 9
+    d = inputs(t, h, rd, gate=gate, gd=F32 if rd == BF else BF)
+    op = ResidualNorm(h, post_weight=d["post"], pre_weight=d["pre"], residual_dtype=rd)
+    r, n = op.forward(d["x"], d["r"], gate=d["g"])
+    for cut in (slice(0, k), slice(t - k, t)):          # the batch's ends, each by itself
+        g = d["g"][cut].clone() if gate in ("token", "full") else d["g"]
+        r2, n2 = op.forward(d["x"][cut].clone(), d["r"][cut].clone(), gate=g)
+        assert torch.equal(r[cut], r2) and torch.equal(n[cut], n2)
+
+
 def test_same_bits_again_on_another_stream_and_in_a_graph():
     h = 2048
     d = inputs(50, h, gate="channel")

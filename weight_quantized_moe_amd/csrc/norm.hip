@@ -274,7 +274,23 @@ static void norm_launch(const NormArgs &a, int64_t T, int threads, hipStream_t s
 // in flight at once (16384 rows of 2048: 51 us; 16 a lane 54, 32 a lane, one wave a
 // row, 60).  Rows of up to 512 share a workgroup, of up to 256 a wave (50000 rows
 // of 128: 25.7 -> 17.0 us).
-hipError_t launch_norm(const NormArgs &a, int64_t T, hipStream_t s) {
+hipError_t launch_norm(const NormArgs &all, int64_t rows, hipStream_t s) {
+  // a grid holds fewer than 2^32 lanes, 2^21 rows at most 2^31
+  constexpr int64_t kMostRows = 1 << 21;
+  NormArgs a = all;
+  for (; rows > kMostRows; rows -= kMostRows) {
+    const hipError_t e = launch_norm(a, kMostRows, s);
+    if (e != hipSuccess) return e;
+    const int64_t n = kMostRows * a.H;
+    auto after = [](const void *p, int64_t bytes) { return p ? (const char *)p + bytes : nullptr; };
+    if (a.x) a.x += n;
+    a.residual = after(a.residual, n * (a.r_bf16 ? 2 : 4));
+    if (a.gate_kind != MQ_GATE_CHANNEL)
+      a.gate = after(a.gate, (a.gate_kind == MQ_GATE_FULL ? n : kMostRows) * (a.gate_bf16 ? 2 : 4));
+    a.residual_out = (void *)after(a.residual_out, n * (a.r_bf16 ? 2 : 4));
+    if (a.norm_out) a.norm_out += n;
+  }
+  const int64_t T = rows;
   const int eights = (a.H + 7) / 8;
   if (eights <= 16)
     norm_launch<1, 16>(a, T, 256, s);
