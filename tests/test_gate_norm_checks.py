@@ -251,3 +251,34 @@ def test_norm_oracle():
     x = np.array([[3.0, 4.0]])
     r, add = onorm.residual_update(x, None, post_weight=[1.0, 2.0], eps=1e-12, scale=0.5, gate=[[2.0]])
     assert np.allclose(add, [[3 / math.sqrt(12.5), 8 / math.sqrt(12.5)]]) and np.all(r == 0)
+
+
+@pytest.mark.parametrize("e,h,i,k", [(8, 256, 128, 2), (128, 2048, 768, 8), (512, 128, 128, 1), (16, 256, 128, 16)])
+def test_the_gate_takes_no_workspace_of_its_own(lib, e, h, i, k):
+    """A workspace of the size that the layer needed before it had a gate is
+    enough: its arrays, each rounded up to 256 bytes, are these."""
+    d = LayerDesc(1, e, h, i, k, 2, P, P + 0x1000, None, P + 0x2000, P + 0x3000, None)
+    handle, n = ctypes.c_void_p(), ctypes.c_size_t()
+    assert lib.moe_quant_init(ctypes.byref(d), ctypes.byref(handle)) == OK
+
+    def size(t):
+        assert lib.moe_quant_workspace_size(handle, t, ctypes.byref(n)) == OK
+        return n.value
+
+    assert size(0) > 0
+    chunks = 256 * e * 4
+    for t in (1, 2, 17, 64, 65, 300, 4096, 100000):
+        r = t * k
+        parts = (16, 4 * r, 4 * r, 4 * (e + 1), 16 * (e + 1), 16 * r, 4 * (e + 1), 4 * (e + 1), 4 * r, 4 * r, chunks,
+                 2 * t * h, 4 * t, 4 * t * e, 2 * r * i, 2 * r * h)
+        assert size(t) <= sum(-(-p // 256) * 256 for p in parts), t
+    lib.moe_quant_destroy(handle)
+
+
+def test_noalloc_takes_as_many_tokens_as_before(lib):
+    d = LayerDesc(1, 8, 256, 128, 2, 2, P, P + 0x1000, None, P + 0x2000, P + 0x3000, None)
+    handle, n = ctypes.c_void_p(), ctypes.c_size_t()
+    assert lib.moe_quant_init(ctypes.byref(d), ctypes.byref(handle)) == OK
+    assert lib.moe_quant_workspace_size(handle, 31237, ctypes.byref(n)) == OK
+    assert n.value <= 64 << 20
+    lib.moe_quant_destroy(handle)

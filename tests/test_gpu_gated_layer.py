@@ -349,3 +349,17 @@ def test_two_threads():
     for th in threads:
         th.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("t", [1, 3, 17, 300])
+def test_the_workspace_is_all_it_takes(t):
+    """A workspace of exactly the stated size between bytes that stay as they were."""
+    lay = GpuLayer(*random_layer("fp8_b128", 7, 16, 256, 128), 4)
+    d = make(t, 16, 256, seed=t)
+    gate, n = gate_of(16, 4, d["bias"], **GROUPED), lay.layer.workspace_size(t)
+    around = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    for call in (lambda **kw: lay.layer.forward_gated(gate, d["x"], logits=d["lg"], **kw),
+                 lambda **kw: lay.layer.forward(d["lg"], d["x"], **kw)):
+        out, ref = call(workspace=around[4096:4096 + n]), call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and bool((around[:4096] == 0xA5).all()) and bool((around[4096 + n:] == 0xA5).all())

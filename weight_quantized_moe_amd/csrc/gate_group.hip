@@ -50,7 +50,6 @@ __device__ __forceinline__ void group_few(const int32_t *ids, const float *wts, 
   for (int j = 0; j < R; ++j) rank += __builtin_amdgcn_readlane(e, j) < e && ((firsts >> j) & 1ull);
   if (lane < R) {
     const int pos = below + earlier, t = lane / k;
-    q.sorted_slots[pos] = lane;
     q.rowinfo[pos] = int4{lane, t, __builtin_bit_cast(int, rowscale ? rowscale[t] : 0.f),
                           __builtin_bit_cast(int, wts[lane])};
     q.inv_pos[lane] = pos;
@@ -104,7 +103,7 @@ __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void 
     return;
   }
   group_small_body<512>(s_ids, s_wts, scales ? s_rs : nullptr, a.T, g.E, g.k, q.offsets, q.mtile, q.einfo, q.rcp,
-                        q.sorted_slots, q.rowinfo, q.inv_pos, q.p_offsets, q.p_sorted_tok, q.p_inv, s_ids);
+                        q.rowinfo, q.inv_pos, q.p_offsets, q.p_sorted_tok, q.p_inv, s_ids);
 }
 
 hipError_t launch_gate_group(const GateArgs &g, const void *logits, int bf16, const GateOut &o, const StageArgs &a,

@@ -18,7 +18,7 @@ struct StageArgs {
 struct GroupArgs {
   int32_t *offsets, *mtile;
   int4 *einfo;
-  int32_t *rcp, *sorted_slots;
+  int32_t *rcp;
   int4 *rowinfo;
   int32_t *inv_pos, *p_offsets, *p_sorted_tok, *p_inv;
 };

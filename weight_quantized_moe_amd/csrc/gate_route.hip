@@ -57,7 +57,7 @@ hipError_t launch_route_gated(const LayerDims &L, const FwdPtrs &P, const Worksp
                  P.flags, P.act_g13};
   if (route_groups(L, P, decode)) {
     const GroupArgs q = {(int32_t *)(ws + W.offsets), (int32_t *)(ws + W.mtile), (int4 *)(ws + W.active),
-                         (int32_t *)(ws + W.rcpre), (int32_t *)(ws + W.sorted_slots), (int4 *)(ws + W.rowinfo),
+                         (int32_t *)(ws + W.rcpre), (int4 *)(ws + W.rowinfo),
                          (int32_t *)(ws + W.inv_pos), P.p_offsets, P.p_sorted_tok, P.p_inv};
     return launch_gate_group(*P.gated, logits, bf16, o, a, q, s);
   }

@@ -67,7 +67,7 @@ struct Workspace {
   size_t rowinfo;              // int4 [R]: {slot, token, row scale bits, routing weight bits} per grouped row
   size_t mtile;                // int32 [E+1]: prefix of ceil(n_e / kPrefillBM)
   size_t rcpre;                // int32 [E+1]: per active expert, prefix of its 16-row chunks ceil(n_e / 16)
-  size_t sorted_slots;         // int32 [R]: slot t*k+j of each grouped row
+  size_t wscale;               // float [T]: gated routing, the power of two taken out of a token's weights
   size_t inv_pos;              // int32 [R]
   size_t x16;                  // fp16 [T, H]: hidden rows scaled by 2^-s_t (INT4: k order of the unpack)
   size_t rowscale;             // float [T]: 2^s_t
@@ -75,7 +75,6 @@ struct Workspace {
   size_t h;                    // fp16 [R, I]
   size_t partial;              // fp16 [R, H]: routing-weighted expert outputs per slot
   size_t chunks;               // int32 [kMaxChunks, E]: per-chunk expert counts, then bases
-  size_t wscale;               // float [T]: gated routing, the power of two taken out of a token's weights
   size_t flags;                // uint32 [4] at offset 0: bit 0 = an FP16 intermediate saturated
   size_t total;
 };

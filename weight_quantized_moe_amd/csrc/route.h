@@ -435,7 +435,7 @@ template <int NTH>
 __device__ __forceinline__ void group_small_body(
     const int32_t *ids, const float *wts, const float *rowscale, int T, int E, int k,
     int32_t *__restrict__ offsets, int32_t *__restrict__ mtile, int4 *__restrict__ einfo,
-    int32_t *__restrict__ rcp, int32_t *__restrict__ sorted_slots, int4 *__restrict__ rowinfo,
+    int32_t *__restrict__ rcp, int4 *__restrict__ rowinfo,
     int32_t *__restrict__ inv_pos, int32_t *__restrict__ p_offsets, int32_t *__restrict__ p_sorted_tok,
     int32_t *__restrict__ p_inv, int32_t *sm_ids) {
   __shared__ uint64_t mask[kMaxExperts * (kSmallT / 64)];  // [E][NW]
@@ -465,7 +465,6 @@ __device__ __forceinline__ void group_small_body(
     const uint64_t below = tb == 0 ? 0ull : (~0ull >> (64 - tb));
     int pos = off[e] + __popcll(mask[e * NW + tw] & below);
     for (int w = 0; w < tw; ++w) pos += __popcll(mask[e * NW + w]);
-    sorted_slots[pos] = i;
     const float rs = rowscale ? rowscale[tt] : 0.f;
     rowinfo[pos] = int4{i, tt, __builtin_bit_cast(int, rs), __builtin_bit_cast(int, wts[i])};
     inv_pos[i] = pos;

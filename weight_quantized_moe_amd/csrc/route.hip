@@ -261,12 +261,11 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_route_kernel(
 __global__ __launch_bounds__(1024) void group_small_kernel(
     const int32_t *__restrict__ ids, const float *__restrict__ wts, const float *__restrict__ rowscale,
     int T, int E, int k, int32_t *__restrict__ offsets, int32_t *__restrict__ mtile,
-    int4 *__restrict__ einfo, int32_t *__restrict__ rcp, int32_t *__restrict__ sorted_slots,
-    int4 *__restrict__ rowinfo,
+    int4 *__restrict__ einfo, int32_t *__restrict__ rcp, int4 *__restrict__ rowinfo,
     int32_t *__restrict__ inv_pos, int32_t *__restrict__ p_offsets, int32_t *__restrict__ p_sorted_tok,
     int32_t *__restrict__ p_inv) {
   __shared__ int32_t sm_ids[kSmallRows];
-  group_small_body<1024>(ids, wts, rowscale, T, E, k, offsets, mtile, einfo, rcp, sorted_slots, rowinfo,
+  group_small_body<1024>(ids, wts, rowscale, T, E, k, offsets, mtile, einfo, rcp, rowinfo,
                          inv_pos, p_offsets, p_sorted_tok, p_inv, sm_ids);
 }
 
@@ -286,7 +285,7 @@ __global__ __launch_bounds__(256) void route_group_kernel(
     int32_t *__restrict__ ids, float *__restrict__ wts, float *__restrict__ rowscale,
     uint32_t *__restrict__ flags, int32_t *__restrict__ p_ids, float *__restrict__ p_w, int with_scales,
     int32_t *__restrict__ offsets, int32_t *__restrict__ mtile, int4 *__restrict__ einfo,
-    int32_t *__restrict__ rcp, int32_t *__restrict__ sorted_slots, int4 *__restrict__ rowinfo,
+    int32_t *__restrict__ rcp, int4 *__restrict__ rowinfo,
     int32_t *__restrict__ inv_pos, int32_t *__restrict__ p_offsets, int32_t *__restrict__ p_sorted_tok,
     int32_t *__restrict__ p_inv) {
   __shared__ int32_t s_ids[kFusedT * 64];
@@ -332,7 +331,7 @@ __global__ __launch_bounds__(256) void route_group_kernel(
   }
   if (with_scales && threadIdx.x < T) rowscale[threadIdx.x] = s_rs[threadIdx.x];
   group_small_body<256>(s_ids, s_wts, with_scales ? s_rs : nullptr, T, E, k, offsets, mtile, einfo, rcp,
-                        sorted_slots, rowinfo, inv_pos, p_offsets, p_sorted_tok, p_inv, s_ids);
+                        rowinfo, inv_pos, p_offsets, p_sorted_tok, p_inv, s_ids);
 }
 
 // ---------------------------------------------------------------------------
@@ -407,9 +406,8 @@ __global__ __launch_bounds__(1024) void scan_kernel(int32_t *__restrict__ cnt, i
 __global__ __launch_bounds__(256) void scatter_kernel(
     const int32_t *__restrict__ ids, const float *__restrict__ wts,
     const float *__restrict__ rowscale, int T, int E, int k, int chunk,
-    const int32_t *__restrict__ base, int32_t *__restrict__ sorted_slots,
-    int4 *__restrict__ rowinfo, int32_t *__restrict__ inv_pos, int32_t *__restrict__ p_sorted_tok,
-    int32_t *__restrict__ p_inv) {
+    const int32_t *__restrict__ base, int4 *__restrict__ rowinfo, int32_t *__restrict__ inv_pos,
+    int32_t *__restrict__ p_sorted_tok, int32_t *__restrict__ p_inv) {
   extern __shared__ __align__(16) unsigned char smem[];
   uint64_t *mask = (uint64_t *)smem;              // [4][E]
   int32_t *wbase = (int32_t *)(mask + 4 * E);     // [4][E]
@@ -441,7 +439,6 @@ __global__ __launch_bounds__(256) void scatter_kernel(
         const int e = ids[(size_t)t * k + j];
         const int pos = wbase[wave * E + e] + __popcll(mask[wave * E + e] & below);
         const int slot = t * k + j;
-        sorted_slots[pos] = slot;
         const float rs = rowscale ? rowscale[t] : 0.f;
         rowinfo[pos] = int4{slot, t, __builtin_bit_cast(int, rs), __builtin_bit_cast(int, wts[slot])};
         inv_pos[slot] = pos;
@@ -488,7 +485,7 @@ static hipError_t route_group_dispatch(const LayerDims &L, const FwdPtrs &P, con
                      (int32_t *)(ws + W.topk_ids), (float *)(ws + W.topk_w), (float *)(ws + W.rowscale),
                      P.flags, P.p_ids, P.p_w, stage_rows == 2 ? 1 : 0, (int32_t *)(ws + W.offsets),
                      (int32_t *)(ws + W.mtile), (int4 *)(ws + W.active), (int32_t *)(ws + W.rcpre),
-                     (int32_t *)(ws + W.sorted_slots), (int4 *)(ws + W.rowinfo), (int32_t *)(ws + W.inv_pos),
+                     (int4 *)(ws + W.rowinfo), (int32_t *)(ws + W.inv_pos),
                      P.p_offsets, P.p_sorted_tok, P.p_inv);
   return hipGetLastError();
 }
@@ -567,8 +564,7 @@ hipError_t launch_permute(const LayerDims &L, const FwdPtrs &P, const Workspace 
     hipLaunchKernelGGL(group_small_kernel, dim3(1), dim3(1024), 0, s, (const int32_t *)(ws + W.topk_ids),
                        (const float *)(ws + W.topk_w), decode && L.H > kRowRegsMaxH ? (const float *)nullptr : (const float *)(ws + W.rowscale),
                        P.T, L.E, L.k, (int32_t *)(ws + W.offsets), (int32_t *)(ws + W.mtile),
-                       (int4 *)(ws + W.active), (int32_t *)(ws + W.rcpre), (int32_t *)(ws + W.sorted_slots),
-                       (int4 *)(ws + W.rowinfo),
+                       (int4 *)(ws + W.active), (int32_t *)(ws + W.rcpre), (int4 *)(ws + W.rowinfo),
                        (int32_t *)(ws + W.inv_pos), P.p_offsets, P.p_sorted_tok, P.p_inv);
     return hipGetLastError();
   }
@@ -583,8 +579,7 @@ hipError_t launch_permute(const LayerDims &L, const FwdPtrs &P, const Workspace 
   hipLaunchKernelGGL(scatter_kernel, dim3(nc), dim3(256), (size_t)L.E * (4 * 8 + 4 * 4 + 4), s,
                      (const int32_t *)(ws + W.topk_ids), (const float *)(ws + W.topk_w),
                      decode && L.H > kRowRegsMaxH ? nullptr : (const float *)(ws + W.rowscale), P.T, L.E, L.k, chunk,
-                     (const int32_t *)cnt, (int32_t *)(ws + W.sorted_slots),
-                     (int4 *)(ws + W.rowinfo), (int32_t *)(ws + W.inv_pos), P.p_sorted_tok,
+                     (const int32_t *)cnt, (int4 *)(ws + W.rowinfo), (int32_t *)(ws + W.inv_pos), P.p_sorted_tok,
                      P.p_inv);
   return hipGetLastError();
 }
