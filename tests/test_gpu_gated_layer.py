@@ -363,3 +363,14 @@ def test_the_workspace_is_all_it_takes(t):
         out, ref = call(workspace=around[4096:4096 + n]), call()
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and bool((around[:4096] == 0xA5).all()) and bool((around[4096 + n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("e", [2, 63, 64, 65, 300, 511, 512])
+@pytest.mark.parametrize("t,k", [(1, 2), (3, 2), (16, 1), (13, 4), (16, 4), (8, 8)])
+def test_few_slots_and_any_number_of_experts(e, t, k):
+    """Up to 64 slots are grouped beside the gate: tables of E + 1 entries, whose
+    last pass over the experts a workgroup takes with few lanes or one."""
+    k = min(k, e)
+    lay = GpuLayer(*random_layer("nvfp4_g16", 9, e, 128, 128), k)
+    d = make(t, e, 128, seed=t + e)
+    check(lay, gate_of(e, k, d["bias"], score="sigmoid"), dict(score="sigmoid"), d)

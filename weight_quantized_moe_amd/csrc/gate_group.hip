@@ -34,16 +34,20 @@ __device__ __forceinline__ void group_few(const int32_t *ids, const float *wts, 
   }
   const uint64_t firsts = __ballot(lane < R && earlier == 0);
   const int active = __popcll(firsts);
-  for (int x = tid; x <= E; x += 512) {
+  // every lane of a wave stays for the counting, also past E: the slots are read from all of them
+  for (int x0 = __builtin_amdgcn_readfirstlane(tid & ~63); x0 <= E; x0 += 512) {
+    const int x = x0 + lane;
     int rows = 0, experts = 0;
     for (int j = 0; j < R; ++j) {
       const bool lower = __builtin_amdgcn_readlane(e, j) < x;
       rows += lower;
       experts += lower && ((firsts >> j) & 1ull);
     }
-    q.offsets[x] = rows;
-    if (q.p_offsets) q.p_offsets[x] = rows;
-    q.mtile[x] = experts;
+    if (x <= E) {
+      q.offsets[x] = rows;
+      if (q.p_offsets) q.p_offsets[x] = rows;
+      q.mtile[x] = experts;
+    }
   }
   if (tid >= 64) return;
   int rank = 0;  // active experts below this one
