@@ -181,3 +181,23 @@ def test_same_bits_again_on_another_stream_and_in_a_graph():
         r4, n4 = op.forward(d["x"], d["r"], gate=d["g"])
         torch.cuda.synchronize()
         assert torch.equal(r3, r4) and torch.equal(n3, n4)
+
+
+@pytest.mark.parametrize("h", [5, 256, 333, 8192, 16384])
+@pytest.mark.parametrize("rd", [BF, F32])
+def test_two_calls_give_the_bits_of_one_for_zeros_too(h, rd):
+    """Zeros of either sign in the block's output and in the residual: without x
+    the residual comes back as it is."""
+    d = inputs(8, h, rd)
+    d["x"][:4], d["x"][2] = -0.0, 0.0
+    d["r"][::2], d["r"][1, ::2] = -0.0, 0.0
+    whole = torch.int16 if rd == BF else torch.int32
+    for scale in (1.0, -0.5):
+        kw = dict(residual_dtype=rd, scale=scale)
+        r, n = ResidualNorm(h, post_weight=d["post"], pre_weight=d["pre"], **kw).forward(d["x"], d["r"])
+        r1, _ = ResidualNorm(h, post_weight=d["post"], **kw).forward(d["x"], d["r"])
+        r2, n2 = ResidualNorm(h, pre_weight=d["pre"], **kw).forward(None, r1)
+        torch.cuda.synchronize()
+        assert torch.equal(r.view(whole), r1.view(whole)) and torch.equal(r.view(whole), r2.view(whole))
+        assert torch.equal(n.view(torch.int16), n2.view(torch.int16))
+    assert bool(torch.signbit(r).any())

@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_kernel(NormArgs a, i
       if (a.pre_w) load_pre(j);
     }
   }
-  float scale = a.scale;
+  float scale = a.x ? a.scale : -0.f;  // no x: r + -0 is r, a zero's sign with it
   if (a.gate_kind == MQ_GATE_TOKEN)
     scale *= a.gate_bf16 ? bf16_to_f32(((const uint16_t *)a.gate)[t]) : ((const float *)a.gate)[t];
   Row8 v[R];
