@@ -201,3 +201,12 @@ def test_two_calls_give_the_bits_of_one_for_zeros_too(h, rd):
         assert torch.equal(r.view(whole), r1.view(whole)) and torch.equal(r.view(whole), r2.view(whole))
         assert torch.equal(n.view(torch.int16), n2.view(torch.int16))
     assert bool(torch.signbit(r).any())
+
+
+@pytest.mark.parametrize("gd", [BF, F32])
+def test_a_per_token_gate_begins_at_any_of_its_elements(gd):
+    """Tokens from the second on: also where a row is one value, so that a factor
+    per token and a factor per value have the same shape."""
+    for h in (1, 8, 77):
+        d = inputs(9, h, gate="token", gd=gd)
+        check(8, h, dict(d, x=d["x"][1:].clone(), r=d["r"][1:].clone(), g=d["g"][1:]))

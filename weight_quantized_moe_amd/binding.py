@@ -501,7 +501,7 @@ class ResidualNorm:
         kind, gate_dtype, gate_ptr = GATE_NONE, MQ_F32, None
         if gate is not None:
             gs = gate.shape
-            kind = (GATE_CHANNEL if gs == (h,) else GATE_FULL if gs == shape else GATE_TOKEN if gs == (t, 1) else None)
+            kind = (GATE_CHANNEL if gs == (h,) else GATE_TOKEN if gs == (t, 1) else GATE_FULL if gs == shape else None)
             if kind is None:
                 raise ValueError(f"gate has shape {tuple(gs)}, expected ({h},), ({t}, 1) or ({t}, {h})")
             gate_dtype, gate_ptr = _mq_dtype(gate.dtype), gate.data_ptr()
