@@ -271,3 +271,28 @@ def test_same_bits_again_on_another_stream_and_in_a_graph():
         i4, w4 = g.topk(x)
         torch.cuda.synchronize()
         assert torch.equal(i3, i4) and torch.equal(w3, w4)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [6, 17])
+def test_raw_weights_keep_their_digits_far_from_zero(score, k):
+    """The exponent of a far logit is exact: a sigmoid's is the logit itself, and
+    these softmaxes' logits are multiples of 2^-10 below a maximum of 0.  What is
+    left, in units of 2^-24: 2 for the power and 2 for the reciprocal (one unit in
+    their last place), 1 each for the power's correction, the product, the scale
+    and the reference's own cast, the denominator's 1 + exp(-|l|) 2 (a rounding,
+    and |l| exp(-|l|) log2 e of the power at most 0.53); a softmax's sum over 24
+    experts takes at most 24 additions in place of those 2, and its terms' powers,
+    off by |a| exp(-|a|) log2 e + 2, weighted by themselves, at most 3: 10, 36."""
+    e, t = 24, 400
+    gen = np.random.default_rng(3)
+    lg = gen.uniform(-85.0, 20.0, (t, e)).astype(np.float32)
+    if score == "softmax":
+        lg = np.round(lg * 1024 * 0.8).clip(-81920, 0).astype(np.float32) / 1024
+        lg[:, 5] = 0.0
+    ids, w = Gate(e, k, score=score, renormalize=False, scale=1.5).topk(torch.from_numpy(lg).cuda())
+    torch.cuda.synchronize()
+    ref_ids, ref = ogate.gate(lg.astype(np.float64), k, score, renormalize=False, scale=1.5)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    off = np.abs(w.cpu().numpy().astype(np.float64) - ref) / ref
+    assert off.max() <= (10 if score == "sigmoid" else 36) * 2.0 ** -24, off.max() * 2.0 ** 24

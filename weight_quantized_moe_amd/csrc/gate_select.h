@@ -30,6 +30,8 @@ namespace mq {
 constexpr float kInf = __builtin_inff();
 constexpr float kMost = 3.402823466e38f;  // the largest finite value
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
+constexpr float kLn2 = 0.693147180559945309417f;
 
 // Order-preserving map of a double to an unsigned integer; -0 maps to the key
 // of +0, and no key of a number is 0 (the key of a selected or excluded expert).
@@ -64,12 +66,19 @@ __device__ __forceinline__ float max64f(float v) {
 // renormalised); m and z: softmax maximum and sum over all experts.  Written so
 // that nothing overflows and small scores keep their digits: sigmoid(l) =
 // exp(min(l, 0)) / (1 + exp(-|l|)), a renormalised row shifted by its largest.
-// The hardware's exp2 and reciprocal are off by a unit in the last place, the
-// exponent by 2^-23 |l|: the weight by a few 2^-24 beside that.
+// The hardware's exp2 and reciprocal are off by a unit in the last place.  The
+// exponent x log2 e is a 32-bit product and its remainder, which corrects the
+// power: a product alone is off by up to 2^-24 |x| log2 e, and the weight by as
+// much.  What is left is the rounding of x itself where it is a difference, and
+// in the denominator, which is 1 and more, a quarter of 2^-24 |l| exp(-|l|).
 __device__ __forceinline__ float slot_score(const GateArgs &g, float l, float top, float m, float z) {
   const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
   const float down = sigmoid ? (g.renormalize ? fminf(top, 0.f) : 0.f) : g.renormalize ? top : m;
-  float s = __builtin_amdgcn_exp2f(((sigmoid ? fminf(l, 0.f) : l) - down) * kLog2e);
+  // exp(-200) is 0; the remainder of a product that overflows would be no number
+  const float x = fmaxf((sigmoid ? fminf(l, 0.f) : l) - down, -200.f), p = x * kLog2e;
+  const float rest = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -p));
+  float s = __builtin_amdgcn_exp2f(p);
+  s = fmaf(s * rest, kLn2, s);
   if (sigmoid)
     s *= __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(fabsf(l) * -kLog2e));
   else if (!g.renormalize)
