@@ -296,3 +296,36 @@ def test_raw_weights_keep_their_digits_far_from_zero(score, k):
     assert np.array_equal(ids.cpu().numpy(), ref_ids)
     off = np.abs(w.cpu().numpy().astype(np.float64) - ref) / ref
     assert off.max() <= (10 if score == "sigmoid" else 36) * 2.0 ** -24, off.max() * 2.0 ** 24
+
+
+def test_the_largest_array_in_32_bits():
+    """The most tokens and experts there may be: 2^31 logits, the last at element
+    2^31 - 1 and past byte 2^33."""
+    t, e, k = 1 << 22, 512, 3
+    lg = torch.zeros((t, e), device="cuda")
+    rows = torch.tensor([0, 1, 5, t // 4, t // 2 + 1, t - 2, t - 1], device="cuda")
+    lg[rows] = logits(len(rows), e)
+    ids, w = Gate(e, k, score="sigmoid", bias=a_bias(e)).topk(lg)
+    ref_ids, ref_w = ogate.gate(as_f64(lg[rows]), k, "sigmoid", bias=as_f64(a_bias(e)))
+    assert np.array_equal(ids[rows].cpu().numpy(), ref_ids)
+    assert np.allclose(w[rows].cpu().numpy(), ref_w, rtol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e,t0", [(128, 3), (65, 8), (511, 16), (48, 5)])
+def test_rows_from_the_middle_of_larger_arrays(dtype, e, t0):
+    """Logits, ids and weights that begin and end inside larger arrays, as a prompt
+    in chunks gives them: what lies around the outputs stays."""
+    t, k = 21, 5
+    lg, bias = logits(64, e, dtype=dtype), a_bias(e)
+    lg[:t0], lg[t0 + t:] = 100.0, 100.0
+    g = Gate(e, k, score="sigmoid", bias=bias)
+    ids = torch.full((64, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((64, k), -7.0, device="cuda")
+    cut = slice(t0, t0 + t)
+    g.topk(lg[cut], ids=ids[cut], weights=w[cut])
+    torch.cuda.synchronize()
+    ref_ids, ref_w = ogate.gate(as_f64(lg[cut]), k, "sigmoid", bias=as_f64(bias))
+    assert np.array_equal(ids[cut].cpu().numpy(), ref_ids) and np.allclose(w[cut].cpu().numpy(), ref_w, rtol=1e-5)
+    for a in (ids, w):
+        assert bool((a[:t0] == -7).all()) and bool((a[t0 + t:] == -7).all())

@@ -374,3 +374,134 @@ def test_few_slots_and_any_number_of_experts(e, t, k):
     lay = GpuLayer(*random_layer("nvfp4_g16", 9, e, 128, 128), k)
     d = make(t, e, 128, seed=t + e)
     check(lay, gate_of(e, k, d["bias"], score="sigmoid"), dict(score="sigmoid"), d)
+
+
+SIGMOID8 = dict(score="sigmoid", groups=8, topk_groups=4, group_top=2, scale=2.5)
+
+
+@pytest.mark.parametrize("t", [9, 16, 61])
+@pytest.mark.parametrize("e,k,kw", [
+    (64, 8, dict(score="sigmoid")), (64, 8, SIGMOID8), (128, 8, dict(score="softmax")), (128, 8, SIGMOID8),
+    (192, 8, SIGMOID8), (256, 8, dict(score="sigmoid", renormalize=False)), (256, 8, SIGMOID8),
+    (384, 8, dict(score="softmax", groups=16, topk_groups=7)), (380, 9, dict(score="softmax", renormalize=False)),
+    (512, 8, dict(score="sigmoid")), (512, 16, SIGMOID8),
+    (48, 6, dict(score="sigmoid", groups=3, topk_groups=2, group_top=2)),      # no number of groups for four tokens a wave
+    (48, 17, dict(score="softmax")), (512, 33, dict(score="sigmoid", groups=32, topk_groups=9, scale=0.25)),
+    (96, 64, dict(score="softmax", scale=16.0)),
+])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_every_gate_in_front_of_the_experts(t, e, k, kw, dtype):
+    """The gate's variants beside the grouping (up to 16 tokens, with more than 64
+    slots) and beside the rows' staging."""
+    lay = GpuLayer(*random_layer("int4_g128", 9, e, 128, 128), k)
+    d = make(t, e, 128, seed=t + e)
+    d["lg"] = d["lg"].to(dtype)
+    bias = d["bias"] if kw["score"] == "sigmoid" or k == 9 else None
+    check(lay, gate_of(e, k, bias, **kw), kw, d)
+
+
+def check_activations(lay, kw, d, bias, g13=None, g2=None):
+    """W8A8, or with global scales W4A4: the intermediate's values against the
+    oracle's before it rounds them, and the output against the oracle's from the
+    intermediate that came back, to the layer's tolerance.  The output is not held
+    to the oracle's own intermediate: a step of E4M3 is up to 2^-3 of the value, so
+    where one slot has nearly all of a token's weight the 1 in 100 of its values that
+    may differ by a step move the output by up to 2^-3 sqrt(1 / 100) = 1.3e-2, more
+    than the layer's tolerance.  E4M3: half a step, 2^-4 of the value or of the least
+    normal number 2^-6, and 0.05 (twice 448 times the 5e-5 that the FP8 matrix unit's
+    sums are off by).  E2M1: 1 in 100 of n values may differ, a spread of
+    sqrt(n / 100), 5 of which are allowed for."""
+    from oracle import codecs, formats, w4a4, w8a8
+    t, k, i = d["x"].shape[0], lay.top_k, lay.layer.inter
+    pr = dict(probe_for(t, lay), h=torch.empty((t * k, i), dtype=torch.float16, device="cuda"))
+    act = dict(activations="fp8") if g13 is None else dict(activations="nvfp4", act_gscale13=g13, act_gscale2=g2)
+    gate, ws = gate_of(lay.layer.num_experts, k, bias, **kw), lay.layer.workspace(t)
+    out = lay.layer.forward_gated(gate, d["x"], logits=d["lg"], probe=pr, workspace=ws, **act)
+    torch.cuda.synchronize()
+    assert not lay.layer.check(ws)
+    ids, w = ogate.gate(f64(d["lg"]), k, bias=None if bias is None else f64(bias), **kw)
+    assert np.array_equal(pr["topk_ids"].cpu().numpy(), ids)
+    assert np.allclose(f64(pr["topk_w"]), w, rtol=1e-5, atol=1e-30)
+    perm = omoe.permute(ids, lay.layer.num_experts)
+    assert np.array_equal(pr["inv_pos"].cpu().numpy(), perm.inv_pos)
+    x = f64(d["x"])
+    if g13 is None:
+        hb = pr["h"].cpu().numpy().view(np.uint8).reshape(-1)
+        n = t * k * i
+        codes, scales = hb[:n].reshape(t * k, i), hb[n:n + n // 32].view(np.float32).reshape(t * k, i // 128)
+        h = w8a8.dequantize_act(codes, scales)
+        xq = w8a8.dequantize_act(*w8a8.quantize_act(x))
+    else:
+        h = f64(pr["h"]) / np.float64(np.float32(g2))
+        xq = w4a4.quantize_dequantize(x, g13)
+    forced, h32 = np.empty((t * k, lay.layer.hidden)), np.empty((t * k, i), np.float32)
+    for e in range(lay.layer.num_experts):
+        lo, hi = perm.offsets[e], perm.offsets[e + 1]
+        if hi > lo:
+            w13, w2 = formats.dequantize_expert(lay.p13, e), formats.dequantize_expert(lay.p2, e)
+            forced[lo:hi] = h[lo:hi] @ w2.T
+            gu = xq[perm.sorted_token_ids[lo:hi]] @ w13.T
+            h32[lo:hi] = omoe.silu(gu[:, :i]) * gu[:, i:]
+    if g13 is None:
+        ref = w8a8.quantize_act(h32)[1]
+        assert np.allclose(scales, ref, rtol=2.0 ** -12, atol=0)
+        q = h32 / np.repeat(ref, 128, axis=1)
+        off = np.abs(codecs.decode_e4m3(codes) - q) - 2.0 ** -4 * np.maximum(np.abs(q), 2.0 ** -6)
+        assert off.max() <= 0.05, off.max()
+    else:
+        differ = (np.abs(h - w4a4.quantize_dequantize(h32, g2)) > 1e-6 * np.abs(h)).sum()
+        assert differ <= h.size / 100 + 5 * np.sqrt(h.size / 100), (differ, h.size)
+    y = omoe.combine(perm, w, forced)
+    rel = np.linalg.norm(f64(out) - y) / np.linalg.norm(y)
+    assert rel <= RTOL_L2, rel
+
+
+WEIGHTS = {
+    "above one": (GROUPED, 0.0), "far above one": (dict(GROUPED, scale=300.0), 0.0),
+    "small": (dict(score="sigmoid", scale=2.0 ** -40), 0.0),
+    "raw and small": (dict(score="sigmoid", renormalize=False), -40.0),
+    "raw softmax": (dict(score="softmax", renormalize=False, scale=2.0 ** -9), 0.0),
+}
+
+
+@pytest.mark.parametrize("t", [1, 9, 40, 300])
+@pytest.mark.parametrize("weights", list(WEIGHTS))
+def test_fp8_and_nvfp4_activations_under_weights_of_any_size(t, weights):
+    """Groups, sigmoids and biases in front of the W8A8 and W4A4 paths, with weights
+    that a power of two is taken out of."""
+    from oracle import w4a4
+    kw, shift = WEIGHTS[weights]
+    d = make(t, 16, 256, seed=t)
+    d["lg"] = d["lg"] + shift
+    bias = d["bias"] if kw["score"] == "sigmoid" and shift == 0.0 else None
+    check_activations(GpuLayer(*random_layer("fp8_b128", 7, 16, 256, 128), 4), kw, d, bias)
+    lay = GpuLayer(*random_layer("nvfp4_g16", 7, 16, 256, 128), 4)
+    g13 = 448 * 6 / float(d["x"].float().abs().max())
+    g2 = 448 * 6 / float(np.abs(w4a4.intermediate_w4a4(lay.oracle, f64(d["lg"]), bits(d["x"]), g13)).max())
+    check_activations(lay, kw, d, bias, g13, g2)
+
+
+@pytest.mark.parametrize("t", [3, 12, 40, 300])
+@pytest.mark.parametrize("scale", [2.5, 2.0 ** -40])
+def test_scaled_rows_saturate_where_a_power_of_two_says(t, scale):
+    """Renormalised weights of a quarter times a scale: above 1 or far below 2^-7
+    their largest is brought to [1/2, 1), so expert outputs of up to 65504 fit and
+    twice that times 5/8 does not."""
+    p13, p2 = random_layer("fp8_b128", 7, 16, 256, 128)
+    d = make(t, 16, 256, seed=t)
+    d["lg"] = torch.zeros_like(d["lg"])
+    lay = GpuLayer(p13, p2, 4)
+    alone = [oracle_layer(lay, np.full((t, 1), e, np.int32), np.ones((t, 1)), bits(d["x"]))[0] for e in range(4)]
+    kw, big = dict(score="softmax", scale=4 * scale), np.abs(alone).max()
+    scales = p2.scale.copy()
+    w = scale * 2.0 ** -np.floor(np.log2(scale) + 1)            # the weight without its power of two
+    for factor, saturated in ((0.95 * 65504 / w / big, False), (1.1 * 65504 / w / big, True)):
+        p2.scale[:] = scales * factor
+        lay = GpuLayer(p13, p2, 4)
+        ws = lay.layer.workspace(t)
+        out = lay.layer.forward_gated(gate_of(16, 4, **kw), d["x"], logits=d["lg"], workspace=ws)
+        assert lay.layer.check(ws) == saturated
+        if not saturated:
+            ids, wt = ogate.gate(f64(d["lg"]), 4, **kw)
+            y, _ = oracle_layer(lay, ids, wt, bits(d["x"]))
+            assert np.linalg.norm(f64(out) - y) <= RTOL_L2 * np.linalg.norm(y)

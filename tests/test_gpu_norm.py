@@ -210,3 +210,22 @@ def test_a_per_token_gate_begins_at_any_of_its_elements(gd):
     for h in (1, 8, 77):
         d = inputs(9, h, gate="token", gd=gd)
         check(8, h, dict(d, x=d["x"][1:].clone(), r=d["r"][1:].clone(), g=d["g"][1:]))
+
+
+@pytest.mark.parametrize("h,t0", [(2048, 3), (1023, 8), (77, 16), (8, 1), (16392, 2)])
+@pytest.mark.parametrize("rd", [BF, F32])
+def test_rows_from_the_middle_of_larger_arrays(h, t0, rd):
+    """Rows that begin and end inside larger arrays: as from arrays of their own,
+    and what lies around the outputs stays."""
+    d, t = inputs(40, h, rd, gate="full", seed=h), 13
+    cut = slice(t0, t0 + t)
+    own = {n: (v[cut].clone() if n in ("x", "r", "g") else v) for n, v in d.items()}
+    r, n = check(t, h, own, rd=rd, scale=0.5)
+    op = ResidualNorm(h, post_weight=d["post"], pre_weight=d["pre"], residual_dtype=rd, scale=0.5)
+    ro = torch.full((40, h), 7.0, dtype=rd, device="cuda")
+    no = torch.full((40, h), 7.0, dtype=BF, device="cuda")
+    op.forward(d["x"][cut], d["r"][cut], gate=d["g"][cut], residual_out=ro[cut], norm_out=no[cut])
+    torch.cuda.synchronize()
+    assert torch.equal(ro[cut], r) and torch.equal(no[cut], n)
+    for a in (ro, no):
+        assert bool((a[:t0] == 7.0).all()) and bool((a[t0 + t:] == 7.0).all())
