@@ -406,9 +406,12 @@ mq_status moe_quant_gate_topk(const mq_gate *g, const void *logits, int32_t logi
  *   logits_out     NULL, or float [T, E] that receives the logits computed here
  *   the others     as for moe_quant_forward; masked logits (-inf, NaN) are those
  *                  of mq_gate
- * The per-slot expert outputs are rounded to FP16.  Where a token's largest
- * weight is above 1 or below 2^-7, a power of two is taken out of its weights
- * first, so weights of any size keep their digits.
+ * The per-slot products of weight and expert output are rounded to FP16, which
+ * has all of its digits between 2^-14 and 65504.  Where a token's largest weight
+ * is above 1 or below 2^-7, a power of two that brings it to [1/2, 1) is taken out
+ * of its weights first and multiplied back after the sum, so the size of the
+ * weights costs no digits; largest weights from 2^-7 to 1 are taken as they are,
+ * as moe_quant_forward takes its own.
  * A layer of one expert with top_k 1, MQ_SCORE_SIGMOID and renormalize 0 is a
  * shared expert with its sigmoid gate.
  * Errors: as moe_quant_forward and moe_quant_gate_topk, MQ_E_NULL unless

@@ -7,15 +7,6 @@
 
 namespace mq {
 
-// ---------------------------------------------------------------------------
-// Decode batches of up to kFusedT tokens: gate, powers of two of the hidden rows
-// and grouping in one workgroup (route_group_kernel's counterpart): waves 0 to 3
-// take the gate of 4 tokens each, waves 4 to 7 their rows' powers of two, and
-// all of them the grouping on the ids and weights in LDS.  One token of 128
-// experts: 5.1 us, bound by the latency of its steps; in three launches the
-// layer's step took 23.2 us, with this one 18.6, with group_few 18.2, with the
-// gate's modes fixed at compile time 17.7.
-// ---------------------------------------------------------------------------
 // Grouping of R = T k <= 64 slots (T <= kFusedT) without a barrier: lane i is slot
 // i in every wave, and a slot's row is the number of slots before it in the order
 // (expert, slot), counted over the slots.  No expert has more than kFusedT rows:
@@ -70,6 +61,15 @@ __device__ __forceinline__ void group_few(const int32_t *ids, const float *wts, 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Decode batches of up to kFusedT tokens: gate, powers of two of the hidden rows
+// and grouping in one workgroup (route_group_kernel's counterpart): waves 0 to 3
+// take the gate of 4 tokens each, waves 4 to 7 their rows' powers of two, and
+// all of them the grouping on the ids and weights in LDS.  One token of 128
+// experts: 5.1 us, bound by the latency of its steps; in three launches the
+// layer's step took 23.2 us, with this one 18.6, with group_few 18.2, with the
+// gate's modes fixed at compile time 17.7 (17.2 to 17.5 on other cards).
+// ---------------------------------------------------------------------------
 template <int kPer, GateMode kMode, bool kWhole>
 __global__ __launch_bounds__(512) void gate_group_kernel(GateArgs g, const void *__restrict__ logits, int bf16,
                                                          GateOut o, StageArgs a, GroupArgs q) {

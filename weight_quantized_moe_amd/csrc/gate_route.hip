@@ -14,8 +14,8 @@ namespace mq {
 // (1), the powers of two alone (2), FP8 codes and scales (3), NVFP4 values (4),
 // nothing (0).  Also clears the saturation flag.  Beside each other in one launch
 // the two take the longer one's time: 4096 tokens of 128 experts and 2048 values
-// 10.6 us (32 MB of rows: 3.2 TB/s), the layer 429 -> 417 us; 61 tokens 5.4 us,
-// the layer 113 -> 106 us.
+// 10.8 us (32 MB of rows: 3.1 TB/s), 61 tokens 5.0 us.  Against two launches, on one
+// card: the layer 429 -> 417 us and 113 -> 106 us (424 and 104 on another).
 // ---------------------------------------------------------------------------
 template <int kPer, GateMode kMode, bool kWhole>
 __global__ __launch_bounds__(256) void gate_stage_kernel(GateArgs g, const void *__restrict__ logits, int bf16,

@@ -8,12 +8,12 @@
 // on 32-bit ones, bounds their error and looks again, in 64 bits, where the
 // order lies within it.
 //
-// Measured (sigmoid, bias, k 8, 32-bit logits): 65536 tokens of 128 experts 18.0
-// us (2.1 TB/s), 16384 of 256 in 8 groups, 4 kept, 11.4 us (1.6 TB/s); all in 64
-// bits, a wave a token, 69 and 38 us.  Bound by vector instructions: 501 a wave
-// of four tokens of 128 experts, issued in 75% of the kernel's cycles (867 of 256
-// with groups); finding close scores and the 64-bit second looks take 1.9 us of
-// the 18.0, 1.4 of the 11.4.  Loops over several groups of four tokens a wave
+// Measured (sigmoid, bias, k 8, 32-bit logits): 65536 tokens of 128 experts 17.8
+// to 18.4 us (2.1 TB/s), 16384 of 256 in 8 groups, 4 kept, 10.1 to 11.3 us (1.7
+// TB/s); all in 64 bits, a wave a token, 69 and 38 us.  Bound by vector
+// instructions: 506 a wave of four tokens of 128 experts, issued in 76% of the
+// kernel's cycles (876 of 256 with groups); finding close scores and the 64-bit
+// second looks take 1.9 us of the first and 1.4 of the second.  Loops over several groups of four tokens a wave
 // were slower (26 against 19 us: more registers).
 #pragma once
 #include <hip/hip_runtime.h>
@@ -94,8 +94,8 @@ __device__ __forceinline__ float over_sum(float s, float sum) {
 
 // The exponent of the power of two that brings a token's largest weight m into
 // [2^-1, 1); 0 (none) for 2^-7 to 1, where every renormalised row of up to 64
-// slots lies: such a row's products saturate in FP16 no earlier than under the
-// layer's own routing.
+// slots lies if the scale is 1: such a row's products have the range in FP16 that
+// they have under the layer's own routing (digits from 2^-14 on, saturation).
 __device__ __forceinline__ int weight_exponent(float m) {
   if (!(m > 0.f) || (m >= 0x1p-7f && m <= 1.f)) return 0;
   const int ex = (int)(__builtin_bit_cast(uint32_t, m) >> 23) - 126;
@@ -607,7 +607,10 @@ __device__ __forceinline__ uint32_t gate_tokens4(const GateArgs &g, const void *
   uint32_t lo = least(tau);
   int n = at_least(lo), have = sum16i(n);
   if (__any(have > kFastK)) {
-    // too many for the lanes: tau goes up to the next key while k are left
+    // too many for the lanes: tau goes up to the next key while k are left.  A key
+    // a round, and all of the kept groups' keys from the least on where their lanes'
+    // two largest are fewer than k: 16384 tokens of 256 experts, k 8, 1 of 8 groups
+    // kept (two lanes a group) 28.5 us, 4 kept 11.1; 512, 1 of 16 kept 48, 8 kept 18
     bool more = have > kFastK;
     while (__any(more)) {
       uint32_t up = 0xFFFFFFFFu;
@@ -744,6 +747,9 @@ __device__ __forceinline__ void gate_wave(const GateArgs &g, const void *__restr
 }
 
 // Calls f with the kernel variant for this gate: f(kPer, mode, kWhole) as constants.
+// kPer is the least of 4, 8, 12, 16, 24 and 32 that holds a lane's experts.  12 and
+// 24 beside the powers of two (16384 tokens, sigmoid and bias): 192 experts 9.0 us,
+// in lanes of 16 11.0; 384 12.0, in lanes of 32 22.3; 160 in 8 groups 10.4 and 11.6.
 template <typename F>
 static hipError_t with_gate_variant(const GateArgs &g, F f) {
   using std::integral_constant;
