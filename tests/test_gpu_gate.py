@@ -329,3 +329,18 @@ def test_rows_from_the_middle_of_larger_arrays(dtype, e, t0):
     assert np.array_equal(ids[cut].cpu().numpy(), ref_ids) and np.allclose(w[cut].cpu().numpy(), ref_w, rtol=1e-5)
     for a in (ids, w):
         assert bool((a[:t0] == -7).all()) and bool((a[t0 + t:] == -7).all())
+
+
+@pytest.mark.parametrize("e,k,groups,topk_groups", [(12, 4, 1, 1), (64, 4, 1, 1), (64, 17, 1, 1), (64, 8, 8, 3), (48, 6, 3, 2)])
+def test_sigmoids_as_small_as_64_bits_hold(e, k, groups, topk_groups):
+    """Logits of -735 to -700 half a unit apart: their sigmoids are subnormal numbers
+    in 64 bits, in the logits' order."""
+    gen = np.random.default_rng(11)
+    lg = np.stack([gen.permutation(70)[:e] for _ in range(30)]).astype(np.float32) * 0.5 - 735.0
+    for top in (1, 2) if groups > 1 else (1,):
+        g = Gate(e, k, score="sigmoid", bias=torch.zeros(e, device="cuda"), num_groups=groups, topk_groups=topk_groups,
+                 group_top=top)
+        ids, _ = g.topk(torch.from_numpy(lg).cuda())
+        ref, _ = ogate.gate(lg.astype(np.float64), k, "sigmoid", bias=np.zeros(e), groups=groups,
+                            topk_groups=topk_groups, group_top=top)
+        assert np.array_equal(ids.cpu().numpy(), ref)

@@ -152,7 +152,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
   for (int i = 0; i < kPer; ++i) {
     c[i] = l[i];
     if (scores || (!sigmoid && !g.renormalize)) {
-      c[i] = exp(sigmoid ? -(double)l[i] : (double)l[i] - (double)m);
+      c[i] = exp(sigmoid ? -fabs((double)l[i]) : (double)l[i] - (double)m);
       z += c[i];
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -168,7 +168,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &g, const void *__rest
     const int e = lane + 64 * i;
     const bool live = l[i] > -kInf && b[i] > -kInf;
     double s = l[i];
-    if (scores) s = (sigmoid ? 1.0 / (1.0 + c[i]) : c[i] / z) + (double)b[i];
+    if (scores) s = (sigmoid ? (l[i] < 0.f ? c[i] : 1.0) / (1.0 + c[i]) : c[i] / z) + (double)b[i];
     if (!live) s = -kInf;
     if (g.groups > 1 && e < g.E) sc[e] = s;
     key[i] = e < g.E ? ordered_key64(by_logit ? (double)l[i] : s) : 0ull;
@@ -326,11 +326,12 @@ __device__ __forceinline__ void top2_joind(double &a, double &b) {
   b = fmax(fmin(a, c), fmax(b, d));
   a = fmax(a, c);
 }
-// A selection score in 64 bits (live experts; zd: the softmax's sum).
+// A selection score in 64 bits (live experts; zd: the softmax's sum).  A sigmoid by
+// exp(-|l|), which does not overflow: exp(-l) would leave 0 below -709.
 __device__ __forceinline__ double wide_score(const GateArgs &g, float l, float m, double zd, int e) {
   const bool sigmoid = g.score == MQ_SCORE_SIGMOID;
-  const double p = exp(sigmoid ? -(double)l : (double)l - (double)m);
-  return (sigmoid ? 1.0 / (1.0 + p) : p / zd) + (g.bias ? (double)gate_logit(g.bias[e]) : 0.0);
+  const double p = exp(sigmoid ? -fabs((double)l) : (double)l - (double)m);
+  return (sigmoid ? (l < 0.f ? p : 1.0) / (1.0 + p) : p / zd) + (g.bias ? (double)gate_logit(g.bias[e]) : 0.0);
 }
 // The softmax's sum over a row's experts in 64 bits.
 template <int kPer>
