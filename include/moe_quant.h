@@ -479,6 +479,158 @@ mq_status moe_quant_norm(const mq_norm *n, const uint16_t *x_bf16, const void *r
                          void *residual_out, uint16_t *norm_out_bf16, struct ihipStream_t *stream);
 
 /*
+ * Matrix product on E4M3 weights with a scale for each block of 128: a dense
+ * projection in the formats of the FP8 layer's forward_w8a8 (its shared or
+ * dense layers, the projections around the attention).
+ *   sa[t, g] = max |x[t, k]| * (1 / 448) over the k of block g = k / 128, an FP32
+ *              product with the FP32 number next to 1 / 448 (1 where that is 0),
+ *   a[t, k]  = RNE-to-E4M3(x[t, k] / sa[t, g]) saturated to +-448, one IEEE FP32
+ *              division,
+ *   y[t, n]  = sum_g sa[t, g] * scale[n / 128, g] * sum_{k in g} a[t, k] * w[n, k],
+ *   out      = round(y + residual) to out_dtype,
+ * sums in FP32.  For an FP32 output the products of codes are exact; for a BF16
+ * one they come from the FP8 matrix units, which cut the 128 products of a block
+ * at 2^-16 of their largest (an error of 6e-5 of it in the mean).  N and K need
+ * not fill their last block.  A weight code of NaN (0x7F, 0xFF) makes
+ * its output column NaN; x must be finite.
+ */
+typedef struct {
+  uint32_t abi_version; /* must equal MOE_QUANT_ABI_VERSION                          */
+  int32_t n;            /* N output features, 1 to 2^20                                */
+  int32_t k;            /* K input features, a multiple of 16, 16 to 65536             */
+  int32_t out_dtype;    /* mq_dtype of out                                             */
+  const uint8_t *w;     /* E4M3FN bits [N, K], 16-byte aligned                         */
+  const float *scale;   /* [ceil(N / 128), ceil(K / 128)], 4-byte aligned              */
+} mq_linear;
+
+/*
+ * Device workspace bytes of moe_quant_linear over num_tokens tokens (the
+ * activation codes and their scales).  Host only.
+ */
+mq_status moe_quant_linear_workspace_size(const mq_linear *l, int64_t num_tokens, size_t *bytes);
+
+/*
+ * Enqueue the product of num_tokens rows on `stream`.
+ *   x_bf16        [T, K] BF16 bits, 16-byte aligned
+ *   residual_bf16 NULL, or [T, N] BF16 bits, 2-byte aligned; may alias out
+ *   out           [T, N] of out_dtype, aligned to its element
+ *   workspace     >= moe_quant_linear_workspace_size bytes, 256-byte aligned; its
+ *                 contents on entry do not matter
+ * num_tokens == 0 returns MQ_OK without enqueuing anything.
+ * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE, MQ_E_DTYPE, MQ_E_ALIGN,
+ * MQ_E_WORKSPACE, MQ_E_HIP.
+ */
+mq_status moe_quant_linear(const mq_linear *l, const uint16_t *x_bf16, const uint16_t *residual_bf16,
+                           int64_t num_tokens, void *out, void *workspace, size_t workspace_bytes,
+                           struct ihipStream_t *stream);
+
+/*
+ * A paged cache of keys and values.  Page p holds page_size tokens of a request,
+ * one head after the other; token s of it is "slot" p * page_size + s, and which
+ * pages a request has, in order, stands in its row of a block table.
+ */
+typedef enum { MQ_KV_BF16 = 0, MQ_KV_FP8 = 1 } mq_kv_dtype;
+
+typedef struct {
+  uint32_t abi_version; /* must equal MOE_QUANT_ABI_VERSION                          */
+  int32_t kv_heads;     /* 1 to 1024                                                   */
+  int32_t head_dim;     /* D, a multiple of 16, 16 to 256                              */
+  int32_t page_size;    /* a power of two, 1 to 1024                                   */
+  int64_t num_pages;    /* at least 1; num_pages * page_size below 2^31                */
+  int32_t dtype;        /* mq_kv_dtype                                                 */
+  float k_scale;        /* MQ_KV_FP8: a key is e4m3 * k_scale, a value e4m3 * v_scale; */
+  float v_scale;        /* finite and positive, 1 for MQ_KV_BF16                       */
+  void *k, *v;          /* [num_pages, kv_heads, page_size, D], 16-byte aligned        */
+} mq_kv_cache;
+
+/*
+ * What happens to a head's query and key before attention, in FP32 and rounded
+ * once at the end:
+ *   h = x,  or with a norm weight  x / sqrt(mean(x^2) + eps) * weight   (mean over D);
+ *   the first rot_dim values of h are turned by the angles of the token's
+ *   position, in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved:
+ *     (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i).
+ * cos_sin [max_positions, rot_dim] holds, for each position, the rot_dim / 2
+ * cosines and then the sines, so any scaling of the angles is the caller's.
+ */
+typedef struct {
+  uint32_t abi_version;  /* must equal MOE_QUANT_ABI_VERSION                         */
+  int32_t head_dim;      /* D of the cache                                             */
+  int32_t rot_dim;       /* 0 (no rotation) or a multiple of 16 up to D                */
+  int32_t interleaved;
+  int32_t max_positions; /* rows of cos_sin; not used if rot_dim is 0                  */
+  float eps;             /* finite and at least 1e-30                                  */
+  const float *cos_sin;  /* 16-byte aligned; NULL if and only if rot_dim is 0          */
+  const uint16_t *q_norm, *k_norm; /* NULL, or [D] BF16 bits, 16-byte aligned          */
+} mq_rotary;
+
+/*
+ * Enqueue, on `stream`, the queries of num_tokens tokens and the appending of
+ * their keys and values to the cache.
+ *   q           [T, q_heads, D] BF16 bits, tokens q_stride values apart, or NULL with
+ *               q_heads 0: no queries
+ *   k, v        [T, kv_heads, D] BF16 bits, tokens k_stride and v_stride values apart
+ *               (so the three may lie in one row of a fused projection); all
+ *               16-byte aligned, strides multiples of 8
+ *   positions   int32 [T]: rows of cos_sin; NULL if rot_dim is 0
+ *   slots       int32 [T]: where the token's key and value go.  A token whose slot
+ *               is negative or behind the cache, or whose position is not a row of
+ *               cos_sin, is padding: nothing of it is written
+ *   q_out       [T, q_heads, D] BF16 bits, 16-byte aligned; may be q itself where
+ *               q_stride is q_heads * D
+ * MQ_KV_FP8 keeps RNE-to-E4M3(value / scale), saturated to +-448.  The slots of
+ * one call are distinct: of a slot given twice it is unspecified which token's
+ * values stay, per 8 values.
+ * num_tokens == 0 returns MQ_OK without enqueuing anything.
+ * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE, MQ_E_DTYPE, MQ_E_ALIGN, MQ_E_HIP.
+ */
+mq_status moe_quant_kv_append(const mq_kv_cache *c, const mq_rotary *r, int32_t q_heads,
+                              const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                              int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                              const int32_t *positions, const int32_t *slots, int64_t num_tokens,
+                              uint16_t *q_out, struct ihipStream_t *stream);
+
+/*
+ * Device workspace bytes of moe_quant_attend over a batch of requests, for any
+ * lengths (256-byte aligned start required).  Host only.
+ */
+mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads, int64_t batch,
+                                          size_t *bytes);
+
+/*
+ * Enqueue, on `stream`, the attention of one new token of each request over the
+ * request's cached tokens (its own among them).  Query head h reads key and
+ * value head h / (q_heads / kv_heads).  For a request of `length` tokens, over
+ * its tokens j < length, with a window only the last `window` of them:
+ *   s_j = scale * q . k_j,   out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j),
+ * statistics and sums in FP32.
+ *   q_bf16      [B, q_heads, D] BF16 bits, 16-byte aligned
+ *   block_table int32, rows table_stride apart: row b holds request b's pages in
+ *               order, max_pages of them at most; what lies behind its last page
+ *               is not read into the result
+ *   lengths     int32 [B]; below 1 the request is empty: out 0, lse -inf.  More
+ *               than max_pages pages hold counts as what they hold
+ *   out_bf16    [B, q_heads, D] BF16 bits, 16-byte aligned; may alias q_bf16
+ *   lse         NULL, or float [B, q_heads], 4-byte aligned
+ *   workspace   >= moe_quant_attend_workspace_size bytes, 256-byte aligned; its
+ *               contents on entry do not matter
+ * Tokens on a page outside of [0, num_pages) count as absent.  What the cache
+ * holds behind a request's last token, NaN among it, does not reach the result;
+ * queries, keys and values of the tokens themselves are finite.  Repeated calls
+ * give the same bits.  batch == 0 returns MQ_OK without enqueuing anything.
+ * Limits: batch at most 65536; q_heads a multiple of kv_heads, at most 1024; scale finite; window 0
+ * (none) or positive; max_pages * page_size below 2^31.
+ * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE, MQ_E_DTYPE, MQ_E_ALIGN,
+ * MQ_E_WORKSPACE, MQ_E_HIP.
+ */
+mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, int32_t window,
+                           const uint16_t *q_bf16, const int32_t *block_table, int64_t table_stride,
+                           int32_t max_pages, const int32_t *lengths, int64_t batch,
+                           uint16_t *out_bf16, float *lse, void *workspace, size_t workspace_bytes,
+                           struct ihipStream_t *stream);
+
+/*
  * Allocation-free variant of moe_quant_forward, for callers that cannot
  * allocate device memory: code under HIP graph capture, tight serving loops,
  * harnesses that forbid allocation.  It runs the same kernels; their scratch

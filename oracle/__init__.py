@@ -15,7 +15,10 @@ of what the GPU path computes:
 * ``moe``     - router top-k + softmax, stable permutation, the per-expert
   SwiGLU loop and the slot-ordered combine;
 * ``gate``    - gated routing (scores, balance bias, groups, top-k, weights);
-* ``norm``    - the norms before and after a block with gate and residual scale.
+* ``norm``    - the norms before and after a block with gate and residual scale;
+* ``linear``  - the dense product on E4M3 weights with a scale per block of 128;
+* ``attention`` - the per-head norm and rotation, and one token's attention over
+  a paged cache.
 
 It shares no code with the GPU path.  Parity of every function is pinned in
 ``tests/test_codecs.py`` and ``tests/test_oracle.py`` against values the model

@@ -8,14 +8,17 @@ library; constructing a :class:`Layer` does, and raises if it is missing.
 from .binding import (  # noqa: F401
     FORMATS,
     Gate,
+    KVCache,
     Layer,
+    Linear,
     MoeQuantError,
     ResidualNorm,
+    Rotary,
     import_expert,
     library_path,
     load_library,
     router_logits,
 )
 
-__all__ = ["FORMATS", "Gate", "Layer", "MoeQuantError", "ResidualNorm", "import_expert", "library_path", "load_library",
-           "router_logits"]
+__all__ = ["FORMATS", "Gate", "KVCache", "Layer", "Linear", "MoeQuantError", "ResidualNorm", "Rotary", "import_expert",
+           "library_path", "load_library", "router_logits"]

@@ -17,6 +17,7 @@ FORMATS = {"int4_g128": 1, "fp8_b128": 2, "nvfp4_g16": 3}
 MQ_F32, MQ_BF16 = 0, 1
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"bf16": 0, "fp8": 1, "nvfp4": 2}
+MQ_KV_BF16, MQ_KV_FP8 = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = range(4)
 STAGES = ("route", "permute", "gate_up", "down", "combine")
 
@@ -31,6 +32,11 @@ EXPORTED = (
     "moe_quant_forward_gated",
     "moe_quant_gate_topk",
     "moe_quant_norm",
+    "moe_quant_linear",
+    "moe_quant_linear_workspace_size",
+    "moe_quant_kv_append",
+    "moe_quant_attend",
+    "moe_quant_attend_workspace_size",
     "moe_quant_quantize_act",
     "moe_quant_quantize_act_nvfp4",
     "moe_quant_import_expert",
@@ -93,6 +99,46 @@ class NormDesc(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("post_weight", ctypes.c_void_p),
         ("pre_weight", ctypes.c_void_p),
+    ]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("w", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+    ]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+    ]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("max_positions", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("cos_sin", ctypes.c_void_p),
+        ("q_norm", ctypes.c_void_p),
+        ("k_norm", ctypes.c_void_p),
     ]
 
 
@@ -172,6 +218,18 @@ def load_library():
     lib.moe_quant_forward_gated.restype = i32
     lib.moe_quant_norm.argtypes = [ctypes.POINTER(NormDesc), vp, vp, vp, i32, i32, i64, vp, vp, vp]
     lib.moe_quant_norm.restype = i32
+    lib.moe_quant_linear_workspace_size.argtypes = [ctypes.POINTER(LinearDesc), i64, ctypes.POINTER(sz)]
+    lib.moe_quant_linear_workspace_size.restype = i32
+    lib.moe_quant_linear.argtypes = [ctypes.POINTER(LinearDesc), vp, vp, i64, vp, vp, sz, vp]
+    lib.moe_quant_linear.restype = i32
+    lib.moe_quant_kv_append.argtypes = [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(RotaryDesc), i32, vp, i64, vp, i64,
+                                        vp, i64, vp, vp, i64, vp, vp]
+    lib.moe_quant_kv_append.restype = i32
+    lib.moe_quant_attend_workspace_size.argtypes = [ctypes.POINTER(KvCacheDesc), i32, i64, ctypes.POINTER(sz)]
+    lib.moe_quant_attend_workspace_size.restype = i32
+    lib.moe_quant_attend.argtypes = [ctypes.POINTER(KvCacheDesc), i32, f32, i32, vp, vp, i64, i32, vp, i64, vp, vp, vp,
+                                     sz, vp]
+    lib.moe_quant_attend.restype = i32
     lib.moe_quant_destroy.argtypes = [vp]
     lib.moe_quant_destroy.restype = None
     lib.moe_quant_status_string.argtypes = [i32]
@@ -539,6 +597,272 @@ class ResidualNorm:
         if st:
             _check(self._lib, st)
         return residual_out, norm_out
+
+
+class Linear:
+    """A dense projection on E4M3 weights with a scale for each block of 128
+    (moe_quant_linear): ``w`` uint8 [N, K] (E4M3FN bits), ``w_scale`` float32
+    [ceil(N / 128), ceil(K / 128)], both on the GPU and alive as long as the object.
+    The rows are quantized to E4M3 per 128 values, as in ``Layer.forward_w8a8``.
+    ``out_dtype``: bfloat16 (default) or float32."""
+
+    def __init__(self, w, w_scale, out_dtype=None):
+        import torch
+        self._lib = load_library()
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"out_dtype {out_dtype}, expected float32 or bfloat16")
+        if w.dim() != 2:
+            raise ValueError("w must be [N, K]")
+        n, k = w.shape
+        _need(w, "w", (n, k), (torch.uint8,))
+        _need(w_scale, "w_scale", (-(-n // 128), -(-k // 128)), (torch.float32,))
+        _on_gpu(None, w=w, w_scale=w_scale)
+        self.n, self.k, self.out_dtype, self.device = n, k, out_dtype, w.device
+        self._keep = (w, w_scale)
+        self._q, self._call, self._index = _get_quick(), self._lib.moe_quant_linear, w.get_device()
+        self.desc = LinearDesc(ABI_VERSION, n, k, _mq_dtype(out_dtype), _ptr(w), _ptr(w_scale))
+        self._ref = ctypes.byref(self.desc)
+        self._last_need = (-1, 0)      # (tokens, bytes) of the last call
+        self.workspace_size(0)         # the library's own checks of the fields
+
+    def workspace_size(self, num_tokens: int) -> int:
+        b = ctypes.c_size_t()
+        _check(self._lib, self._lib.moe_quant_linear_workspace_size(self._ref, num_tokens, ctypes.byref(b)))
+        return b.value
+
+    def _workspace_need(self, num_tokens: int) -> int:
+        last = self._last_need
+        if last[0] != num_tokens:
+            last = self._last_need = (num_tokens, self.workspace_size(num_tokens))
+        return last[1]
+
+    def workspace(self, num_tokens: int):
+        import torch
+        return torch.empty(max(self.workspace_size(num_tokens), 256), dtype=torch.uint8, device=self.device)
+
+    def forward(self, x, residual=None, out=None, workspace=None, stream=None):
+        """``x`` bfloat16 [T, K] -> ``out`` [T, N] = x w^T (+ ``residual``, bfloat16
+        [T, N], which may be ``out`` itself where that is bfloat16)."""
+        q, given, index = self._q, x.shape, self._index
+        if len(given) != 2:
+            raise ValueError("x must be [T, K]")
+        t = given[0]
+        if index != q.device_now():
+            with q.on(index):
+                return self.forward(x, residual, out, workspace, stream)
+        shape, bf16 = (t, self.n), q.bf16
+        if out is None:
+            out = _empty(shape, self.out_dtype, self.device, stream)
+        if workspace is None:
+            workspace = _empty((max(self._workspace_need(t), 256),), q.u8, self.device, stream)
+        if not (_fits(x, (t, self.k), bf16, index) and _fits(out, shape, self.out_dtype, index)
+                and (residual is None or _fits(residual, shape, bf16, index))
+                and workspace.is_contiguous() and workspace.get_device() == index):
+            _need(x, "x", (t, self.k), (bf16,))
+            if residual is not None:
+                _need(residual, "residual", shape, (bf16,))
+            _need(out, "out", shape, (self.out_dtype,))
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            _on_gpu(self.device, x=x, residual=residual, out=out, workspace=workspace)
+        st = self._call(self._ref, x.data_ptr(), None if residual is None else residual.data_ptr(), t, out.data_ptr(),
+                        workspace.data_ptr(), _nbytes(workspace),
+                        q.raw_stream(index) if stream is None else stream.cuda_stream)
+        if st:
+            _check(self._lib, st)
+        return out
+
+
+class Rotary:
+    """What happens to a head's query and key before attention (mq_rotary): the
+    per-head RMS norm (``q_norm``, ``k_norm`` bfloat16 [D], None: none) and the
+    rotation by the position's angles: ``cos_sin`` float32 [positions, R], the R / 2
+    cosines and then the sines of each position (None: no rotation), R a multiple
+    of 16 up to D; pairs (i, i + R / 2), or (2i, 2i + 1) if ``interleaved``.  All on
+    the GPU, alive as long as the object."""
+
+    def __init__(self, head_dim: int, cos_sin=None, interleaved: bool = False, q_norm=None, k_norm=None,
+                 eps: float = 1e-6):
+        import torch
+        if cos_sin is not None:
+            if cos_sin.dim() != 2:
+                raise ValueError("cos_sin must be [positions, R]")
+            _need(cos_sin, "cos_sin", tuple(cos_sin.shape), (torch.float32,))
+            if not 0 < cos_sin.shape[1] <= head_dim or cos_sin.shape[1] % 16:
+                raise ValueError(f"cos_sin has {cos_sin.shape[1]} columns, expected a multiple of 16 up to {head_dim}")
+            if cos_sin.shape[0] < 1:
+                raise ValueError("cos_sin has no positions")
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None:
+                _need(w, name, (head_dim,), (torch.bfloat16,))
+        _on_gpu(None, cos_sin=cos_sin, q_norm=q_norm, k_norm=k_norm)
+        self.head_dim, self.rotates = head_dim, cos_sin is not None
+        self._keep = (cos_sin, q_norm, k_norm)
+        self._index = frozenset(w.get_device() for w in self._keep if w is not None)
+        p, r = cos_sin.shape if self.rotates else (0, 0)
+        self.desc = RotaryDesc(ABI_VERSION, head_dim, r, int(interleaved), min(p, 2 ** 31 - 1), eps, _ptr(cos_sin),
+                               _ptr(q_norm), _ptr(k_norm))
+        self._ref = ctypes.byref(self.desc)
+
+    @staticmethod
+    def table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+        """cos_sin of the angles position * base^(-2i / rot_dim), computed in 64 bits."""
+        import torch
+        rate = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+        angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * rate
+        return torch.cat((angle.cos(), angle.sin()), 1).float()
+
+
+class KVCache:
+    """A paged cache of keys and values (mq_kv_cache): ``k`` and ``v`` [pages,
+    kv_heads, page_size, D], bfloat16 or float8_e4m3fn (then a key is its E4M3
+    value times ``k_scale``, a value times ``v_scale``), on the GPU, alive as long
+    as the object.  Slot p * page_size + s is token s of page p."""
+
+    def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
+        import torch
+        self._lib = load_library()
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, kv_heads, page_size, D]")
+        _need(k, "k", tuple(k.shape), (torch.bfloat16, torch.float8_e4m3fn))
+        _need(v, "v", tuple(k.shape), (k.dtype,))
+        _on_gpu(None, k=k, v=v)
+        pages, heads, page_size, d = k.shape
+        self.k, self.v, self.device = k, v, k.device
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page_size, d
+        self._q, self._index = _get_quick(), k.get_device()
+        self._append, self._attend = self._lib.moe_quant_kv_append, self._lib.moe_quant_attend
+        self.desc = KvCacheDesc(ABI_VERSION, heads, d, page_size, pages,
+                                MQ_KV_BF16 if k.dtype == torch.bfloat16 else MQ_KV_FP8, k_scale, v_scale, _ptr(k),
+                                _ptr(v))
+        self._ref = ctypes.byref(self.desc)
+        self._last_need = (None, 0)             # (batch and query heads, bytes) of the last attend
+        self.attend_workspace_size(0, heads)    # the library's own checks of the fields
+
+    def _heads(self, t, name, tokens, heads):
+        """Token stride of ``t`` [T, heads, D]: heads side by side, tokens any number of values apart."""
+        d = self.head_dim
+        if t.dtype is not self._q.bf16 or t.shape != (tokens, heads, d) or t.get_device() != self._index:
+            if t.dtype is not self._q.bf16:
+                raise ValueError(f"{name} has dtype {t.dtype}, expected {self._q.bf16}")
+            if t.shape != (tokens, heads, d):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
+            _on_gpu(self.device, **{name: t})
+        step, hs, ds = t.stride()
+        if (ds != 1 and d > 1) or (hs != d and heads > 1):
+            raise ValueError(f"the heads of {name} must lie one behind the other")
+        return step if tokens > 1 else heads * d
+
+    def append(self, rotary, q, k, v, positions, slots, q_out=None, stream=None):
+        """Norm and rotate ``q`` bfloat16 [T, q_heads, D] (None: no queries) and ``k``
+        [T, kv_heads, D], and write ``k`` and ``v`` into their ``slots`` (int32 [T];
+        negative: padding, nothing of the token is written).  ``positions`` int32
+        [T] (not used without a rotation).  The heads of a token lie side by side, tokens
+        any multiple of 8 values apart, so all three may be views of one fused
+        projection.  Returns ``q_out`` [T, q_heads, D] (None without queries)."""
+        if k.dim() != 3:
+            raise ValueError("k must be [T, kv_heads, D]")
+        w, index, t = self._q, self._index, k.shape[0]
+        if index != w.device_now():
+            with w.on(index):
+                return self.append(rotary, q, k, v, positions, slots, q_out, stream)
+        ks, vs = self._heads(k, "k", t, self.kv_heads), self._heads(v, "v", t, self.kv_heads)
+        hq, qs, qp, op = 0, 0, None, None
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q must be [T, q_heads, D]")
+            hq = q.shape[1]
+            qs, qp = self._heads(q, "q", t, hq), q.data_ptr()
+            shape = (t, hq, self.head_dim)
+            if q_out is None:
+                q_out = _empty(shape, w.bf16, self.device, stream)
+            elif not _fits(q_out, shape, w.bf16, index):
+                _need(q_out, "q_out", shape, (w.bf16,))
+                _on_gpu(self.device, q_out=q_out)
+            op = q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        pp = None
+        if rotary.rotates:
+            if positions is None or not _fits(positions, (t,), w.i32, index):
+                _need(positions, "positions", (t,), (w.i32,))
+                _on_gpu(self.device, positions=positions)
+            pp = positions.data_ptr()
+        if not _fits(slots, (t,), w.i32, index):
+            _need(slots, "slots", (t,), (w.i32,))
+            _on_gpu(self.device, slots=slots)
+        if not rotary._index <= {index}:
+            _on_gpu(self.device, **dict(zip(("cos_sin", "q_norm", "k_norm"), rotary._keep)))
+        st = self._append(self._ref, rotary._ref, hq, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, pp, slots.data_ptr(), t,
+                          op, w.raw_stream(index) if stream is None else stream.cuda_stream)
+        if st:
+            _check(self._lib, st)
+        return q_out
+
+    def attend_workspace_size(self, batch: int, q_heads: int) -> int:
+        b = ctypes.c_size_t()
+        _check(self._lib, self._lib.moe_quant_attend_workspace_size(self._ref, q_heads, batch, ctypes.byref(b)))
+        return b.value
+
+    def _attend_need(self, batch: int, q_heads: int) -> int:
+        last, what = self._last_need, (batch, q_heads)
+        if last[0] != what:
+            last = self._last_need = (what, self.attend_workspace_size(batch, q_heads))
+        return last[1]
+
+    def attend_workspace(self, batch: int, q_heads: int):
+        import torch
+        return torch.empty(max(self.attend_workspace_size(batch, q_heads), 256), dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, block_table, lengths, scale: Optional[float] = None, window: int = 0, out=None, lse=None,
+               workspace=None, stream=None):
+        """Attention of one new token of each request (moe_quant_attend): ``q``
+        bfloat16 [B, q_heads, D] over the first ``lengths`` (int32 [B]) tokens of
+        the pages in ``block_table`` (int32 [B, pages], rows any distance apart),
+        the last ``window`` of them if that is not 0.  ``scale``: D^-1/2 if None.
+        Returns ``out`` (bfloat16 [B, q_heads, D]; may be ``q``); ``lse`` (float32
+        [B, q_heads]) receives the logarithms of the exponentials' sums."""
+        if q.dim() != 3:
+            raise ValueError("q must be [B, q_heads, D]")
+        w, index = self._q, self._index
+        b, hq, d = q.shape
+        if index != w.device_now():
+            with w.on(index):
+                return self.attend(q, block_table, lengths, scale, window, out, lse, workspace, stream)
+        shape = (b, hq, self.head_dim)
+        if out is None:
+            out = _empty(shape, w.bf16, self.device, stream)
+        if workspace is None:
+            workspace = _empty((max(self._attend_need(b, hq), 256),), w.u8, self.device, stream)
+        if block_table.dim() != 2 or block_table.shape[0] != b or (block_table.shape[1] > 1
+                                                                   and block_table.stride(1) != 1):
+            raise ValueError(f"block_table must be [{b}, pages], the pages of a request side by side")
+        pages = block_table.shape[1]
+        apart = block_table.stride(0) if b > 1 else pages
+        if not (_fits(q, shape, w.bf16, index) and _fits(out, shape, w.bf16, index)
+                and block_table.dtype is w.i32 and block_table.get_device() == index
+                and _fits(lengths, (b,), w.i32, index) and (lse is None or _fits(lse, (b, hq), w.f32, index))
+                and workspace.is_contiguous() and workspace.get_device() == index and apart >= pages):
+            _need(q, "q", shape, (w.bf16,))
+            _need(out, "out", shape, (w.bf16,))
+            if block_table.dtype is not w.i32:
+                raise ValueError(f"block_table has dtype {block_table.dtype}, expected {w.i32}")
+            if apart < pages:
+                raise ValueError("the rows of block_table must not overlap")
+            _need(lengths, "lengths", (b,), (w.i32,))
+            if lse is not None:
+                _need(lse, "lse", (b, hq), (w.f32,))
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            _on_gpu(self.device, q=q, out=out, block_table=block_table, lengths=lengths, lse=lse, workspace=workspace)
+        st = self._attend(self._ref, hq, d ** -0.5 if scale is None else scale, window, q.data_ptr(),
+                          block_table.data_ptr(), apart, pages, lengths.data_ptr(), b, out.data_ptr(),
+                          None if lse is None else lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+                          w.raw_stream(index) if stream is None else stream.cuda_stream)
+        if st:
+            _check(self._lib, st)
+        return out
 
 
 class Layer:

@@ -184,6 +184,51 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs &a, int64_t T, hipStream_t s);
 
+// The dense E4M3 product.  codes [T, Kp] and sa [G, T] lie in the workspace,
+// Kp = 128 G being K with its last block filled up by zeros.
+struct LinearArgs {
+  const uint16_t *x, *residual;
+  const uint8_t *w;
+  const float *scale;
+  void *out;
+  uint8_t *codes;
+  float *sa;
+  int64_t T;
+  int N, K, G, out_bf16;
+};
+hipError_t launch_linear(const LinearArgs &a, hipStream_t s);
+
+struct KvAppendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *positions, *slots;
+  const float *cos_sin;
+  const uint16_t *q_norm, *k_norm;
+  uint16_t *q_out;
+  void *kc, *vc;
+  int64_t num_slots, T;
+  int Hq, Hk, D, R, interleaved, max_positions, page_log2, fp8;
+  float eps, k_scale, v_scale;
+};
+constexpr int kMaxHeads = 1024;
+constexpr int64_t kMaxBatch = 1 << 16;  // requests of one attention
+hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
+
+struct AttendArgs {
+  const uint16_t *q;
+  const void *kc, *vc;
+  const int32_t *table, *lengths;
+  int64_t table_stride;
+  uint16_t *out;
+  float *lse;
+  void *ws;
+  int B, Hq, Hk, D, page_log2, num_pages, max_tokens, window;
+  float score_scale;  // scale * k_scale
+  float v_scale;
+};
+size_t attend_workspace(int64_t B, int Hq, int Hk, int D);
+hipError_t launch_attend(const AttendArgs &a, int fp8, hipStream_t s);
+
 // The forward path behind moe_quant_forward and its allocation-free variant:
 // host checks, then the launch sequence on `stream`.  `flags` (nullable) is
 // the saturation word to use instead of the workspace's first word.
