@@ -47,6 +47,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 constexpr int kTile = 32;    // tokens of one step of a wave
 constexpr int kWaves = 4;
+constexpr int kUnitTokens = 512;   // a whole unit per workgroup up to this many tokens
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // One wave's running state: maximum (in base-2 exponents) and sum for head r
@@ -64,68 +65,74 @@ struct Attend {
   static constexpr int VW = FP8 ? VJ / 4 : VJ / 2;      // and their 32-bit words
   static constexpr int KS = DT / 32;                    // products of 32 over D
   static constexpr int KL = FP8 ? DT / 64 : DT / 32;    // 16-byte loads of a key row per lane
+  static constexpr int LD = DT + 4;
+
+  struct Shared {
+    float m[kWaves][16], l[kWaves][16];
+    __align__(16) float o[kWaves][16][LD];
+  };
+  // What a tile takes from memory.
+  struct Frag {
+    u4 k[2][KL];
+    uint32_t v[8][VW];
+    int seen;    // bit i: the lane's token i is there
+  };
 
   // d of the 8 values that operand kk holds on lane group g
   static __device__ __forceinline__ int d_of(int kk, int g) {
     return FP8 ? 64 * (kk >> 1) + 16 * g + 8 * (kk & 1) : 32 * kk + 8 * g;
   }
-
-  // One tile of 32 tokens from token j0 on.
-  static __device__ __forceinline__ void tile(const AttendArgs &a, const u4 *qf, int kh, const int32_t *table, int j0,
-                                              int start, int end, Running<DT> &R) {
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int ps = 1 << a.page_log2, D = a.D;
-    // slot of token j0 + lane % 32, -1 where there is none
+  // slot of token j0 + lane % 32, -1 where there is none
+  static __device__ __forceinline__ int slot_of(const AttendArgs &a, const int32_t *table, int j0, int start, int end) {
+    const int j = j0 + (threadIdx.x & 31);
     int slot = -1;
-    {
-      const int j = j0 + (lane & 31);
-      if (j >= start && j < end) {
-        const int p = table[j >> a.page_log2];
-        if (p >= 0 && p < a.num_pages) slot = (p << a.page_log2) + (j & (ps - 1));
-      }
+    if (j >= start && j < end) {
+      const int p = table[j >> a.page_log2];
+      if (p >= 0 && p < a.num_pages) slot = (p << a.page_log2) + (j & ((1 << a.page_log2) - 1));
     }
-    const bool whole = __all(slot >= 0);
+    return slot;
+  }
+  // Absent tokens read the first row of the cache, values behind D the row's first
+  // ones (their products meet zeros of q, or land in rows of O that are not kept).
+  static __device__ __forceinline__ void load(const AttendArgs &a, int kh, int slot, Frag &f) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     auto row = [&](int s) -> int64_t {
-      s = s < 0 ? 0 : s;  // an absent token reads the first row and is masked
-      return ((((int64_t)(s >> a.page_log2) * a.Hk + kh) << a.page_log2) + (s & (ps - 1))) * D;
+      s = s < 0 ? 0 : s;
+      return ((((int64_t)(s >> a.page_log2) * a.Hk + kh) << a.page_log2) + (s & ((1 << a.page_log2) - 1))) * a.D;
     };
-    u4 kw[2][KL];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t at = row(__shfl(slot, 16 * h + r, 64));
 #pragma unroll
       for (int i = 0; i < KL; ++i) {
-        const int d = FP8 ? 64 * i + 16 * g : 32 * i + 8 * g;
-        kw[h][i] = u4{0u, 0u, 0u, 0u};
-        if (d < D) kw[h][i] = FP8 ? *(const u4 *)((const uint8_t *)a.kc + at + d)
-                                  : *(const u4 *)((const uint16_t *)a.kc + at + d);
+        const int d0 = FP8 ? 64 * i + 16 * g : 32 * i + 8 * g, d = d0 < a.D ? d0 : 0;
+        f.k[h][i] = FP8 ? *(const u4 *)((const uint8_t *)a.kc + at + d) : *(const u4 *)((const uint16_t *)a.kc + at + d);
       }
     }
-    uint32_t vw[8][VW];
-    bool seen[8];
+    const int dv = VJ * r < a.D ? VJ * r : 0;
+    f.seen = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int s = __shfl(slot, (i < 4 ? 4 * g + i : 12 + 4 * g + i), 64);
-      seen[i] = s >= 0;
-      const int64_t at = row(s) + VJ * r;
+      f.seen |= s >= 0 ? 1 << i : 0;
+      const int64_t at = row(s) + dv;
+      const uint32_t *p = FP8 ? (const uint32_t *)((const uint8_t *)a.vc + at) : (const uint32_t *)((const uint16_t *)a.vc + at);
+      if constexpr (VW == 1) {
+        f.v[i][0] = p[0];
+      } else if constexpr (VW == 2) {
+        const u2 v = *(const u2 *)p;
+        f.v[i][0] = v[0]; f.v[i][1] = v[1];
+      } else {
 #pragma unroll
-      for (int w = 0; w < VW; ++w) vw[i][w] = 0u;
-      if (VJ * r < D && seen[i]) {  // absent values are 0 whatever the cache holds there
-        const uint32_t *p = FP8 ? (const uint32_t *)((const uint8_t *)a.vc + at) : (const uint32_t *)((const uint16_t *)a.vc + at);
-        if constexpr (VW == 1) {
-          vw[i][0] = p[0];
-        } else if constexpr (VW == 2) {
-          const u2 v = *(const u2 *)p;
-          vw[i][0] = v[0]; vw[i][1] = v[1];
-        } else {
-#pragma unroll
-          for (int w = 0; w < VW; w += 4) {
-            const u4 v = *(const u4 *)(p + w);
-            vw[i][w] = v[0]; vw[i][w + 1] = v[1]; vw[i][w + 2] = v[2]; vw[i][w + 3] = v[3];
-          }
+        for (int w = 0; w < VW; w += 4) {
+          const u4 v = *(const u4 *)(p + w);
+          f.v[i][w] = v[0]; f.v[i][w + 1] = v[1]; f.v[i][w + 2] = v[2]; f.v[i][w + 3] = v[3];
         }
       }
     }
+  }
+
+  static __device__ __forceinline__ void compute(float c, const u4 *qf, Frag &f, Running<DT> &R) {
     // ---- scores
     f4 s[2];
 #pragma unroll
@@ -135,35 +142,40 @@ struct Attend {
       for (int kk = 0; kk < KS; ++kk) {
         u4 k;
         if constexpr (FP8) {
-          const uint32_t w0 = kw[h][kk >> 1][2 * (kk & 1)], w1 = kw[h][kk >> 1][2 * (kk & 1) + 1];
+          const uint32_t w0 = f.k[h][kk >> 1][2 * (kk & 1)], w1 = f.k[h][kk >> 1][2 * (kk & 1) + 1];
           k = u4{e4m3x2_to_b2<false>(w0), e4m3x2_to_b2<true>(w0), e4m3x2_to_b2<false>(w1), e4m3x2_to_b2<true>(w1)};
         } else {
-          k = kw[h][kk];
+          k = f.k[h][kk];
         }
         s[h] = mfma_bf16(k, qf[kk], s[h]);
       }
     }
-    const float c = a.score_scale * kLog2e;
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * c;
-    if (!whole) {
+    if (!__all(f.seen == 255)) {
+      // absent tokens: no score, and values of 0 whatever the cache holds there
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = seen[i] ? p[i] : -INFINITY;
+      for (int i = 0; i < 8; ++i) {
+        const bool seen = (f.seen >> i) & 1;
+        p[i] = seen ? p[i] : -INFINITY;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) f.v[i][w] = seen ? f.v[i][w] : 0u;
+      }
     }
     float top = p[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = fmaxf(top, p[i]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float m = fmaxf(R.m, top), mm = m == -INFINITY ? 0.f : m;
-    const float f = __builtin_amdgcn_exp2f(R.m - mm);
-    R.m = m;
-    if (__any(f != 1.f)) {
-      R.l *= f;
+    if (__any(top > R.m)) {
+      const float m = fmaxf(R.m, top), e = __builtin_amdgcn_exp2f(R.m - (m == -INFINITY ? 0.f : m));
+      R.m = m;
+      R.l *= e;
 #pragma unroll
-      for (int j = 0; j < VJ; ++j) R.o[j] *= f;
+      for (int j = 0; j < VJ; ++j) R.o[j] *= e;
     }
+    const float mm = R.m == -INFINITY ? 0.f : R.m;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       p[i] = __builtin_amdgcn_exp2f(p[i] - mm);
@@ -181,7 +193,7 @@ struct Attend {
       u4 v[FP8 ? 4 : 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t x = vw[2 * i][w], y = vw[2 * i + 1][w];
+        const uint32_t x = f.v[2 * i][w], y = f.v[2 * i + 1][w];
         if constexpr (FP8) {
           const uint32_t e = __builtin_amdgcn_perm(y, x, 0x05010400u), o = __builtin_amdgcn_perm(y, x, 0x07030602u);
           v[0][i] = e4m3x2_to_b2<false>(e); v[1][i] = e4m3x2_to_b2<true>(e);
@@ -199,86 +211,278 @@ struct Attend {
       }
     }
   }
+
+  // Tiles t0 to t1 of one unit: a request's tokens [start, end) (tile 0 holds token
+  // `start`) and nh query heads from `head` on that share key head kh.  The
+  // workgroup's waves take the tiles in turn; the joined state goes to `part` (max,
+  // sum, O of 16 heads) if that is given, else the result to out and lse.
+  static __device__ __forceinline__ void unit(const AttendArgs &a, Shared &sh, int b, int kh, int64_t head, int nh, int start,
+                                              int end, int t0, int t1, float *part) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15,
+              g = lane >> 4;
+    u4 qf[KS];
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      const int d = d_of(kk, g);
+      qf[kk] = u4{0u, 0u, 0u, 0u};
+      if (d < a.D && r < nh) qf[kk] = *(const u4 *)(a.q + (head + r) * a.D + d);
+    }
+    Running<DT> R;
+    R.m = -INFINITY;
+    R.l = 0.f;
+#pragma unroll
+    for (int j = 0; j < VJ; ++j) R.o[j] = f4{0.f, 0.f, 0.f, 0.f};
+    const int32_t *table = a.table + b * a.table_stride;
+    const float c = a.score_scale * kLog2e;
+    // one tile's loads are in flight while the one before is computed, and the page
+    // numbers of the tile after that
+    const int base = (start / kTile) * kTile, step = kWaves * kTile, stop = base + t1 * kTile;
+    int j = base + (t0 + wave) * kTile;
+    if constexpr (DT > 128) {
+      // registers for one tile only
+      for (; j < stop; j += step) {
+        Frag f;
+        load(a, kh, slot_of(a, table, j, start, end), f);
+        compute(c, qf, f, R);
+      }
+    } else if (j < stop) {
+      Frag f;
+      int slot = slot_of(a, table, j, start, end);
+      load(a, kh, slot, f);
+      if (j + step < stop) slot = slot_of(a, table, j + step, start, end);
+      for (; j + step < stop; j += step) {
+        Frag n;
+        load(a, kh, slot, n);
+        if (j + 2 * step < stop) slot = slot_of(a, table, j + 2 * step, start, end);
+        compute(c, qf, f, R);
+        f = n;
+      }
+      compute(c, qf, f, R);
+    }
+    // ---- the waves' states joined
+    R.l += __shfl_xor(R.l, 16, 64);
+    R.l += __shfl_xor(R.l, 32, 64);
+    __syncthreads();  // the unit before has been read out
+    if (g == 0) {
+      sh.m[wave][r] = R.m;
+      sh.l[wave][r] = R.l;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < VJ; j += 4)
+        *(f4 *)&sh.o[wave][r][VJ * (4 * g + i) + j] = f4{R.o[j][i], R.o[j + 1][i], R.o[j + 2][i], R.o[j + 3][i]};
+    __syncthreads();
+    const int D = a.D, half = D / 2;
+    for (int at = threadIdx.x; at < nh * half; at += 64 * kWaves) {
+      const int n = at / half, d = 2 * (at - n * half);
+      float m = sh.m[0][n];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sh.m[w][n]);
+      const float mm = m == -INFINITY ? 0.f : m;
+      float l = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sh.m[w][n] - mm);
+        l += f * sh.l[w][n];
+        x += f * sh.o[w][n][d];
+        y += f * sh.o[w][n][d + 1];
+      }
+      if (part) {
+        *(float2 *)(part + 32 + n * D + d) = float2{x, y};
+        if (d == 0) {
+          part[n] = m;
+          part[16 + n] = l;
+        }
+      } else {
+        write_out(a, head + n, d, m, l, x, y);
+      }
+    }
+  }
+
+  // Two values of head hd's result from its maximum, sum and O.
+  static __device__ __forceinline__ void write_out(const AttendArgs &a, int64_t hd, int d, float m, float l, float x, float y) {
+    const float f = l > 0.f ? a.v_scale / l : 0.f;
+    *(uint32_t *)(a.out + hd * a.D + d) = (uint32_t)f32_to_bf16_rne(x * f) | ((uint32_t)f32_to_bf16_rne(y * f) << 16);
+    if (a.lse && d == 0) a.lse[hd] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+  }
 };
 
-template <int DT, bool FP8>
-__global__ __launch_bounds__(64 * kWaves) void attend_kernel(AttendArgs a) {
-  using A = Attend<DT, FP8>;
-  constexpr int LD = DT + 4;
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
-  __shared__ __align__(16) float so[kWaves][16][LD];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+// A request's tokens [start, end) and its tiles.
+struct Span {
+  int start, end, tiles;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int length) {
+  Span s;
+  s.end = max(0, min(length, a.max_tokens));
+  s.start = a.window ? max(0, s.end - a.window) : 0;
+  s.tiles = s.end > s.start ? (s.end + kTile - 1) / kTile - s.start / kTile : 0;
+  return s;
+}
+// Query heads of unit kt (of Hk ceil(group / 16)) of a request.
+struct Heads {
+  int kh, nh;
+  int64_t head;
+};
+__device__ __forceinline__ Heads heads_of(const AttendArgs &a, int b, int kt) {
   const int G = a.Hq / a.Hk, ht = (G + 15) / 16;
-  const int unit = blockIdx.x, b = unit / (a.Hk * ht), kt = unit - b * (a.Hk * ht), kh = kt / ht;
-  const int h0 = (kt - kh * ht) * 16, nh = min(16, G - h0);   // heads of the group that this workgroup takes
-  const int64_t head = (int64_t)b * a.Hq + kh * G + h0;
-  const int end = max(0, min(a.lengths[b], a.max_tokens)), start = a.window ? max(0, end - a.window) : 0;
-  u4 qf[A::KS];
-#pragma unroll
-  for (int kk = 0; kk < A::KS; ++kk) {
-    const int d = A::d_of(kk, g);
-    qf[kk] = u4{0u, 0u, 0u, 0u};
-    if (d < a.D && r < nh) qf[kk] = *(const u4 *)(a.q + (head + r) * a.D + d);
-  }
-  Running<DT> R;
-  R.m = -INFINITY;
-  R.l = 0.f;
-#pragma unroll
-  for (int j = 0; j < A::VJ; ++j) R.o[j] = f4{0.f, 0.f, 0.f, 0.f};
-  const int32_t *table = a.table + b * a.table_stride;
-  for (int j0 = (start / kTile + wave) * kTile; j0 < end; j0 += kWaves * kTile) A::tile(a, qf, kh, table, j0, start, end, R);
-  // ---- the waves' states joined
-  R.l += __shfl_xor(R.l, 16, 64);
-  R.l += __shfl_xor(R.l, 32, 64);
-  if (g == 0) {
-    sm[wave][r] = R.m;
-    sl[wave][r] = R.l;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < A::VJ; j += 4)
-      *(f4 *)&so[wave][r][A::VJ * (4 * g + i) + j] = f4{R.o[j][i], R.o[j + 1][i], R.o[j + 2][i], R.o[j + 3][i]};
+  Heads h;
+  h.kh = kt / ht;
+  const int h0 = (kt - h.kh * ht) * 16;
+  h.nh = min(16, G - h0);
+  h.head = (int64_t)b * a.Hq + h.kh * G + h0;
+  return h;
+}
+
+// ---- short requests: a workgroup takes a whole unit
+template <int DT, bool FP8>
+__global__ __launch_bounds__(64 * kWaves, 2) void attend_units_kernel(AttendArgs a) {
+  using A = Attend<DT, FP8>;
+  __shared__ typename A::Shared sh;
+  const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
+  const int b = blockIdx.x / units, kt = blockIdx.x - b * units;
+  const Heads h = heads_of(a, b, kt);
+  const Span s = span_of(a, a.lengths[b]);
+  A::unit(a, sh, b, h.kh, h.head, h.nh, s.start, s.end, 0, s.tiles, nullptr);
+}
+
+// ---- the others: all tiles of all units, one behind the other, in equal shares
+// for a number of workgroups that the card holds at once, so that requests of any
+// lengths keep it busy to the end.  Workgroup w writes what it has of unit u, if
+// that is not all of it, to part w + u: along the shares w or u or both rise by
+// one from part to part, so no two parts are the same.
+constexpr int kShareMin = 8;   // tiles of a share at least (two per wave)
+
+__device__ __forceinline__ int64_t share_of(int64_t total, int groups) {
+  const int64_t s = (total + groups - 1) / groups;
+  return s < kShareMin ? kShareMin : s;
+}
+
+template <int DT, bool FP8>
+__global__ __launch_bounds__(64 * kWaves, 2) void attend_shares_kernel(AttendArgs a, int groups, int64_t *prefix, float *parts) {
+  using A = Attend<DT, FP8>;
+  __shared__ typename A::Shared sh;
+  __shared__ int64_t sum[64 * kWaves], first[2];
+  const int tid = threadIdx.x, N = 64 * kWaves;
+  const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
+  // ---- tiles in front of each request: a thread adds up its run of requests
+  const int run = (a.B + N - 1) / N, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += span_of(a, a.lengths[b]).tiles;
+  sum[tid] = mine;
   __syncthreads();
-  const int D = a.D;
-  for (int at = threadIdx.x; at < nh * (D / 2); at += 64 * kWaves) {
-    const int n = at / (D / 2), d = 2 * (at - n * (D / 2));
-    float m = sm[0][n];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][n]);
-    const float mm = m == -INFINITY ? 0.f : m;
-    float l = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(sm[w][n] - mm);
-      l += f * sl[w][n];
-      x += f * so[w][n][d];
-      y += f * so[w][n][d + 1];
+  for (int d = 1; d < N; d *= 2) {
+    const int64_t v = tid >= d ? sum[tid - d] : 0;
+    __syncthreads();
+    sum[tid] += v;
+    __syncthreads();
+  }
+  const int64_t total = sum[N - 1] * units, share = share_of(total, groups);
+  int64_t at = blockIdx.x * share;
+  int64_t p = sum[tid] - mine;
+  if (blockIdx.x == 0) {
+    // for the joining kernel
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = p;
+      p += span_of(a, a.lengths[b]).tiles;
     }
-    const float f = l > 0.f ? a.v_scale / l : 0.f;
-    *(uint32_t *)(a.out + (head + n) * D + d) = (uint32_t)f32_to_bf16_rne(x * f) | ((uint32_t)f32_to_bf16_rne(y * f) << 16);
-    if (a.lse && d == 0) a.lse[head + n] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+    if (tid == N - 1) prefix[a.B] = sum[N - 1];
+  }
+  if (at >= total) return;
+  p = sum[tid] - mine;
+  if (p * units <= at && at < (p + mine) * units) {
+    int b = b0;
+    for (;; ++b) {
+      const int n = span_of(a, a.lengths[b]).tiles;
+      if (at < (p + n) * units) break;
+      p += n;
+    }
+    first[0] = b;
+    first[1] = p;
+  }
+  __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane((int)first[0]);
+  int64_t left = (total - at < share ? total - at : share), off = at - first[1] * units;
+  Span s = span_of(a, a.lengths[b]);
+  int kt = __builtin_amdgcn_readfirstlane((int)(off / s.tiles));
+  int t = __builtin_amdgcn_readfirstlane((int)(off - (int64_t)kt * s.tiles));
+  while (left > 0) {
+    if (kt == units || s.tiles == 0) {
+      kt = t = 0;
+      s = span_of(a, a.lengths[++b]);
+      continue;
+    }
+    const int n = (int)(left < s.tiles - t ? left : s.tiles - t);
+    const Heads h = heads_of(a, b, kt);
+    const bool whole = n == s.tiles;
+    float *part = parts + (blockIdx.x + (int64_t)b * units + kt) * (32 + 16 * (int64_t)a.D);
+    A::unit(a, sh, b, h.kh, h.head, h.nh, s.start, s.end, t, t + n, whole ? nullptr : part);
+    left -= n;
+    t = 0;
+    ++kt;
   }
 }
 
+// ---- units that several shares hold, and empty ones
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int groups, const int64_t *prefix, const float *parts) {
+  const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
+  const int b = blockIdx.x / units, kt = blockIdx.x - b * units;
+  const Heads h = heads_of(a, b, kt);
+  const int64_t tiles = prefix[b + 1] - prefix[b], at = prefix[b] * units + kt * tiles;
+  const int64_t share = share_of(prefix[a.B] * units, groups);
+  const int64_t w0 = at / share, w1 = tiles ? (at + tiles - 1) / share : w0;
+  if (tiles && w0 == w1) return;
+  const int D = a.D, half = D / 2;
+  const int64_t size = 32 + 16 * (int64_t)D;
+  const float *part = parts + (w0 + blockIdx.x) * size;
+  const int n = (int)(tiles ? w1 - w0 + 1 : 0);
+  for (int i = threadIdx.x; i < h.nh * half; i += 256) {
+    const int r = i / half, d = 2 * (i - r * half);
+    float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+    for (int w = 0; w < n; ++w) {
+      const float *q = part + w * size;
+      const float mw = q[r], top = fmaxf(m, mw), tt = top == -INFINITY ? 0.f : top;
+      const float e = __builtin_amdgcn_exp2f(m - tt), f = __builtin_amdgcn_exp2f(mw - tt);
+      const float2 o = *(const float2 *)(q + 32 + r * D + d);
+      m = top;
+      l = l * e + q[16 + r] * f;
+      x = x * e + o.x * f;
+      y = y * e + o.y * f;
+    }
+    Attend<64, false>::write_out(a, h.head + r, d, m, l, x, y);
+  }
+}
+
+int groups_of() { return 512; }
+
 }  // namespace
 
-size_t attend_workspace(int64_t, int, int, int) { return 256; }
+// [B + 1] tiles in front of each request, then the parts.
+static size_t prefix_bytes(int64_t B) { return ((size_t)(B + 1) * 8 + 255) / 256 * 256; }
+
+size_t attend_workspace(int64_t B, int Hq, int Hk, int D) {
+  const int64_t units = B * Hk * ((Hq / Hk + 15) / 16);
+  return prefix_bytes(B) + (size_t)(groups_of() + units) * (32 + 16 * (size_t)D) * 4;
+}
+
+template <int DT, bool FP8>
+static hipError_t run_attend(const AttendArgs &a, hipStream_t s) {
+  const unsigned units = (unsigned)a.B * a.Hk * ((a.Hq / a.Hk + 15) / 16);
+  if (a.max_tokens <= kUnitTokens) {
+    attend_units_kernel<DT, FP8><<<dim3(units), dim3(64 * kWaves), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  int64_t *prefix = (int64_t *)a.ws;
+  float *parts = (float *)((char *)a.ws + prefix_bytes(a.B));
+  attend_shares_kernel<DT, FP8><<<dim3(groups_of()), dim3(64 * kWaves), 0, s>>>(a, groups_of(), prefix, parts);
+  attend_join_kernel<<<dim3(units), dim3(256), 0, s>>>(a, groups_of(), prefix, parts);
+  return hipGetLastError();
+}
 
 hipError_t launch_attend(const AttendArgs &a, int fp8, hipStream_t s) {
-  const int ht = (a.Hq / a.Hk + 15) / 16;
-  const dim3 grid((unsigned)a.B * a.Hk * ht), block(64 * kWaves);
-  if (a.D <= 64) {
-    if (fp8) attend_kernel<64, true><<<grid, block, 0, s>>>(a);
-    else attend_kernel<64, false><<<grid, block, 0, s>>>(a);
-  } else if (a.D <= 128) {
-    if (fp8) attend_kernel<128, true><<<grid, block, 0, s>>>(a);
-    else attend_kernel<128, false><<<grid, block, 0, s>>>(a);
-  } else {
-    if (fp8) attend_kernel<256, true><<<grid, block, 0, s>>>(a);
-    else attend_kernel<256, false><<<grid, block, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  if (a.D <= 64) return fp8 ? run_attend<64, true>(a, s) : run_attend<64, false>(a, s);
+  if (a.D <= 128) return fp8 ? run_attend<128, true>(a, s) : run_attend<128, false>(a, s);
+  return fp8 ? run_attend<256, true>(a, s) : run_attend<256, false>(a, s);
 }
 
 }  // namespace mq
