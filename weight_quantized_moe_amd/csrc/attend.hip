@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 constexpr int kTile = 32;    // tokens of one step of a wave
 constexpr int kWaves = 4;
-constexpr int kUnitTokens = 512;   // a whole unit per workgroup up to this many tokens
+// Requests that the pieces' plan goes through; a workgroup takes whole units above it.
+constexpr int kPlanBatch = 1024;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // One wave's running state: maximum (in base-2 exponents) and sum for head r
@@ -346,136 +347,146 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_units_kernel(AttendArgs
   A::unit(a, sh, b, h.kh, h.head, h.nh, s.start, s.end, 0, s.tiles, nullptr);
 }
 
-// ---- the others: all tiles of all units, one behind the other, in equal shares
-// for a number of workgroups that the card holds at once, so that requests of any
-// lengths keep it busy to the end.  Workgroup w writes what it has of unit u, if
-// that is not all of it, to part w + u: along the shares w or u or both rise by
-// one from part to part, so no two parts are the same.
-constexpr int kShareMin = 8;   // tiles of a share at least (two per wave)
-
-__device__ __forceinline__ int64_t share_of(int64_t total, int groups) {
-  const int64_t s = (total + groups - 1) / groups;
-  return s < kShareMin ? kShareMin : s;
+// ---- the others: a unit of n tiles goes to k = ceil(n / share) workgroups in equal
+// pieces, share being what a workgroup gets if the tiles of all units are dealt
+// evenly to `groups`.  The lengths are known on the device only: every wave of a
+// workgroup x goes through them (64 a step) for the piece that is number x, and
+// the pieces behind the last one, at most groups + units in all, have nothing to do.
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
+  return v;
 }
+
+struct Plan {
+  int groups, share_min;   // share: at least share_min tiles
+  int *first;              // [B + 1]: number of a request's first piece; of all pieces
+  float *parts;            // per piece, if its unit has others: 16 maxima, 16 sums, O [16, D]
+};
 
 template <int DT, bool FP8>
-__global__ __launch_bounds__(64 * kWaves, 2) void attend_shares_kernel(AttendArgs a, int groups, int64_t *prefix, float *parts) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attend_pieces_kernel(AttendArgs a, Plan plan) {
   using A = Attend<DT, FP8>;
   __shared__ typename A::Shared sh;
-  __shared__ int64_t sum[64 * kWaves], first[2];
-  const int tid = threadIdx.x, N = 64 * kWaves;
-  const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
-  // ---- tiles in front of each request: a thread adds up its run of requests
-  const int run = (a.B + N - 1) / N, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(a, a.lengths[b]).tiles;
-  sum[tid] = mine;
-  __syncthreads();
-  for (int d = 1; d < N; d *= 2) {
-    const int64_t v = tid >= d ? sum[tid - d] : 0;
-    __syncthreads();
-    sum[tid] += v;
-    __syncthreads();
-  }
-  const int64_t total = sum[N - 1] * units, share = share_of(total, groups);
-  int64_t at = blockIdx.x * share;
-  int64_t p = sum[tid] - mine;
-  if (blockIdx.x == 0) {
-    // for the joining kernel
-    for (int b = b0; b < b1; ++b) {
-      prefix[b] = p;
-      p += span_of(a, a.lengths[b]).tiles;
+  const int lane = threadIdx.x & 63, units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
+  auto tiles_of = [&](int b) { return b < a.B ? span_of(a, a.lengths[b]).tiles : 0; };
+  int64_t total = 0;
+  for (int b = 0; b < a.B; b += 64) total += wave_sum(tiles_of(b + lane));
+  total *= units;
+  const int share = (int)max((int64_t)plan.share_min, (total + plan.groups - 1) / plan.groups);
+  int base = 0, found = -1, rel = 0, k = 1;
+  for (int b = 0; b < a.B; b += 64) {
+    const int n = tiles_of(b + lane), mine = b + lane < a.B ? max(1, (n + share - 1) / share) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += v;
     }
-    if (tid == N - 1) prefix[a.B] = sum[N - 1];
-  }
-  if (at >= total) return;
-  p = sum[tid] - mine;
-  if (p * units <= at && at < (p + mine) * units) {
-    int b = b0;
-    for (;; ++b) {
-      const int n = span_of(a, a.lengths[b]).tiles;
-      if (at < (p + n) * units) break;
-      p += n;
+    const int from = base + (upto - mine) * units;
+    if (blockIdx.x == 0 && threadIdx.x < 64 && b + lane < a.B) plan.first[b + lane] = from;
+    const uint64_t here = __ballot(from <= (int)blockIdx.x && (int)blockIdx.x < from + mine * units);
+    if (here) {
+      const int at = __builtin_ctzll(here);
+      found = b + at;
+      rel = blockIdx.x - __shfl(from, at, 64);
+      k = __shfl(mine, at, 64);
     }
-    first[0] = b;
-    first[1] = p;
+    base += __shfl(upto, 63, 64) * units;
   }
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane((int)first[0]);
-  int64_t left = (total - at < share ? total - at : share), off = at - first[1] * units;
-  Span s = span_of(a, a.lengths[b]);
-  int kt = __builtin_amdgcn_readfirstlane((int)(off / s.tiles));
-  int t = __builtin_amdgcn_readfirstlane((int)(off - (int64_t)kt * s.tiles));
-  while (left > 0) {
-    if (kt == units || s.tiles == 0) {
-      kt = t = 0;
-      s = span_of(a, a.lengths[++b]);
-      continue;
-    }
-    const int n = (int)(left < s.tiles - t ? left : s.tiles - t);
-    const Heads h = heads_of(a, b, kt);
-    const bool whole = n == s.tiles;
-    float *part = parts + (blockIdx.x + (int64_t)b * units + kt) * (32 + 16 * (int64_t)a.D);
-    A::unit(a, sh, b, h.kh, h.head, h.nh, s.start, s.end, t, t + n, whole ? nullptr : part);
-    left -= n;
-    t = 0;
-    ++kt;
-  }
-}
-
-// ---- units that several shares hold, and empty ones
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int groups, const int64_t *prefix, const float *parts) {
-  const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
-  const int b = blockIdx.x / units, kt = blockIdx.x - b * units;
+  if (blockIdx.x == 0 && threadIdx.x == 0) plan.first[a.B] = base;
+  if (found < 0) return;
+  const int b = __builtin_amdgcn_readfirstlane(found);
+  k = __builtin_amdgcn_readfirstlane(k);
+  rel = __builtin_amdgcn_readfirstlane(rel);
+  const int kt = rel / k, i = rel - kt * k;
+  const Span s = span_of(a, a.lengths[b]);
   const Heads h = heads_of(a, b, kt);
-  const int64_t tiles = prefix[b + 1] - prefix[b], at = prefix[b] * units + kt * tiles;
-  const int64_t share = share_of(prefix[a.B] * units, groups);
-  const int64_t w0 = at / share, w1 = tiles ? (at + tiles - 1) / share : w0;
-  if (tiles && w0 == w1) return;
-  const int D = a.D, half = D / 2;
+  float *part = plan.parts + blockIdx.x * (32 + 16 * (int64_t)a.D);
+  A::unit(a, sh, b, h.kh, h.head, h.nh, s.start, s.end, (int)((int64_t)s.tiles * i / k), (int)((int64_t)s.tiles * (i + 1) / k),
+          k == 1 ? nullptr : part);
+}
+
+// ---- the pieces of a unit joined, a workgroup per query head: 64 pairs of D (or
+// more, in turn) on each of 4 waves, every wave a fourth of the pieces.
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan plan) {
+  __shared__ float sx[4][64], sy[4][64];
+  const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
+  const int b = blockIdx.x / units, kt = blockIdx.x - b * units, r = blockIdx.y;
+  const int f0 = plan.first[b], k = (plan.first[b + 1] - f0) / units;
+  const Heads h = heads_of(a, b, kt);
+  if (k <= 1 || r >= h.nh) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = a.D;
   const int64_t size = 32 + 16 * (int64_t)D;
-  const float *part = parts + (w0 + blockIdx.x) * size;
-  const int n = (int)(tiles ? w1 - w0 + 1 : 0);
-  for (int i = threadIdx.x; i < h.nh * half; i += 256) {
-    const int r = i / half, d = 2 * (i - r * half);
-    float m = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
-    for (int w = 0; w < n; ++w) {
-      const float *q = part + w * size;
-      const float mw = q[r], top = fmaxf(m, mw), tt = top == -INFINITY ? 0.f : top;
-      const float e = __builtin_amdgcn_exp2f(m - tt), f = __builtin_amdgcn_exp2f(mw - tt);
-      const float2 o = *(const float2 *)(q + 32 + r * D + d);
-      m = top;
-      l = l * e + q[16 + r] * f;
-      x = x * e + o.x * f;
-      y = y * e + o.y * f;
+  const float *part = plan.parts + (f0 + kt * k) * size;
+  float m = -INFINITY, l = 0.f;
+  for (int w = lane; w < k; w += 64) m = fmaxf(m, part[w * size + r]);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
+  const float mm = m == -INFINITY ? 0.f : m;
+  for (int w = lane; w < k; w += 64) l += part[w * size + 16 + r] * __builtin_amdgcn_exp2f(part[w * size + r] - mm);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, 64);
+  for (int d0 = 0; d0 < D; d0 += 128) {
+    const int d = d0 + 2 * lane;
+    float x = 0.f, y = 0.f;
+    if (d < D) {
+#pragma unroll 8
+      for (int w = wave; w < k; w += 4) {
+        const float f = __builtin_amdgcn_exp2f(part[w * size + r] - mm);
+        const float2 o = *(const float2 *)(part + w * size + 32 + r * D + d);
+        x += f * o.x;
+        y += f * o.y;
+      }
     }
-    Attend<64, false>::write_out(a, h.head + r, d, m, l, x, y);
+    __syncthreads();
+    sx[wave][lane] = x;
+    sy[wave][lane] = y;
+    __syncthreads();
+    if (wave == 0 && d < D)
+      Attend<64, false>::write_out(a, h.head + r, d, m, l, (sx[0][lane] + sx[1][lane]) + (sx[2][lane] + sx[3][lane]),
+                                   (sy[0][lane] + sy[1][lane]) + (sy[2][lane] + sy[3][lane]));
   }
 }
 
-int groups_of() { return 512; }
+// Workgroups that the tiles are dealt to: two on each CU, and all their pieces at
+// once, where units are few; with more units, whose lengths may differ by much,
+// smaller pieces so that the last ones end together (512 - units against 1024 -
+// units groups: 16 units of 3100 to 4096 tiles 98 and 110 us; 192 units of 1 to 256
+// tiles 96 and 89 us).  At least 512 for many units, which need few pieces.
+constexpr int kGroupsMost = 1024;
+int groups_of(int64_t units) {
+  if (units <= 64) return 512 - (int)units;
+  return units < 512 ? kGroupsMost - (int)units : 512;
+}
+// Tiles of a piece at least: with few units one per wave (4 units of 32 tiles:
+// 11.4 us, 12.8 with two per wave), with many as much as keeps a unit whole that the
+// other units' workgroups hide (396 units of 32 tiles: 24 us whole, 31 in two).
+int share_min_of(int64_t units) { return units / 8 < 4 ? 4 : units / 8 > 128 ? 128 : (int)(units / 8); }
 
 }  // namespace
 
-// [B + 1] tiles in front of each request, then the parts.
-static size_t prefix_bytes(int64_t B) { return ((size_t)(B + 1) * 8 + 255) / 256 * 256; }
+// [B + 1] numbers of pieces, then the parts.
+static size_t first_bytes(int64_t B) { return ((size_t)(B + 1) * 4 + 255) / 256 * 256; }
 
 size_t attend_workspace(int64_t B, int Hq, int Hk, int D) {
   const int64_t units = B * Hk * ((Hq / Hk + 15) / 16);
-  return prefix_bytes(B) + (size_t)(groups_of() + units) * (32 + 16 * (size_t)D) * 4;
+  return first_bytes(B) + (size_t)(groups_of(units) + units) * (32 + 16 * (size_t)D) * 4;
 }
 
 template <int DT, bool FP8>
 static hipError_t run_attend(const AttendArgs &a, hipStream_t s) {
-  const unsigned units = (unsigned)a.B * a.Hk * ((a.Hq / a.Hk + 15) / 16);
-  if (a.max_tokens <= kUnitTokens) {
+  const int G = a.Hq / a.Hk;
+  const unsigned units = (unsigned)a.B * a.Hk * ((G + 15) / 16);
+  const int share_min = share_min_of(units), groups = groups_of(units);
+  const int most = a.window && a.window < a.max_tokens ? (a.window + 2 * (kTile - 1)) / kTile : (a.max_tokens + kTile - 1) / kTile;
+  if (most <= share_min || a.B > kPlanBatch) {
     attend_units_kernel<DT, FP8><<<dim3(units), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
   }
-  int64_t *prefix = (int64_t *)a.ws;
-  float *parts = (float *)((char *)a.ws + prefix_bytes(a.B));
-  attend_shares_kernel<DT, FP8><<<dim3(groups_of()), dim3(64 * kWaves), 0, s>>>(a, groups_of(), prefix, parts);
-  attend_join_kernel<<<dim3(units), dim3(256), 0, s>>>(a, groups_of(), prefix, parts);
+  const Plan plan = {groups, share_min, (int *)a.ws, (float *)((char *)a.ws + first_bytes(a.B))};
+  attend_pieces_kernel<DT, FP8><<<dim3(groups + units), dim3(64 * kWaves), 0, s>>>(a, plan);
+  attend_join_kernel<<<dim3(units, G < 16 ? G : 16), dim3(256), 0, s>>>(a, plan);
   return hipGetLastError();
 }
 
