@@ -1,16 +1,21 @@
 // The dense E4M3 product: y[t, n] = sum_g sa[t, g] sw[n / 128, g] sum_{k in g} a[t, k] w[n, k].
 //
-// Two launches: the rows' quantization into the workspace, and the product.
-// Both operands of the product are E4M3 codes, so for a BF16 output one 16x16x128
-// FP8 matrix instruction takes the whole inner sum of a block of 128 for 16
-// weight rows and 16 tokens; the block's two scales multiply it in FP32 on the
-// way into the accumulator.  That instruction aligns its 128 products to the
-// largest and cuts them there: on random codes the sum is off by 2^-14 of the
-// largest product in the mean and by 2^-10.8 at most, which a BF16 output does
-// not show (an FP32 one does: 3e-5 of its 2-norm).  For an FP32 output the codes
-// become FP16 values (exact) and go through four 16x16x32 FP16 instructions,
-// whose sums are FP32 ones (2^-23.7 of the largest product in the mean), at half
-// the rate.
+// Both operands are E4M3 codes, so for a BF16 output one 16x16x128 FP8 matrix
+// instruction takes the whole inner sum of a block of 128 for 16 weight rows and
+// 16 tokens; the block's two scales multiply it in FP32 on the way into the
+// accumulator.  That instruction aligns its 128 products to the largest and cuts
+// them there: on random codes the sum is off by 2^-14 of the largest product in
+// the mean and by 2^-10.8 at most, which a BF16 output does not show (an FP32 one
+// does: 3e-5 of its 2-norm).  For an FP32 output the codes become FP16 values
+// (exact) and go through four 16x16x32 FP16 instructions, whose sums are FP32
+// ones (2^-23.7 of the largest product in the mean), at half the rate.
+//
+// Three ways through it:
+//   few tokens     one launch: every workgroup quantizes the rows itself
+//   some           the rows quantized into the workspace, then the weights
+//                  streamed from memory to registers, the axis K over the waves
+//   many           the rows quantized, then tiles of tokens and weight rows
+//                  through LDS
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,6 +27,8 @@ namespace {
 
 typedef int i8v __attribute__((ext_vector_type(8)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+// 16-byte values at any even address (rows of an odd number of values)
+typedef u4 u4_a2 __attribute__((aligned(2)));
 
 // 16 weight rows (a) x 16 tokens (b) x 128 k; E8M0 scale 127 = 2^0 on both.
 // Lane l holds row l % 16 of each operand and the same 32 of the 128 k (any,
@@ -30,35 +37,42 @@ typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ f4 mfma_fp8_16(const i8v &a, const i8v &b, const f4 &c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
-__device__ __forceinline__ i8v join(u4 x, u4 y) {
-  return i8v{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-}
 
-__device__ __forceinline__ h8 half8(u4 c, int hi) { return unpack_fp8(c[2 * hi], c[2 * hi + 1]); }
-
-// The inner sum of a block of 128: a = (a0, a1), b = (b0, b1) the lane's 32 codes.
+// A lane's 32 codes of a row and a block of 128, as its products take them.
 template <bool kExact>
-__device__ __forceinline__ f4 block_sum(u4 a0, u4 a1, u4 b0, u4 b1) {
-  f4 p = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (kExact) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) p = mfma16(half8(a0, i), half8(b0, i), p);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) p = mfma16(half8(a1, i), half8(b1, i), p);
-    return p;
-  } else {
-    return mfma_fp8_16(join(a0, a1), join(b0, b1), p);
+struct Frag;
+template <>
+struct Frag<false> {
+  i8v v;
+  __device__ __forceinline__ void set(u4 x, u4 y) {
+    v = i8v{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
   }
+};
+template <>
+struct Frag<true> {
+  h8 v[4];
+  __device__ __forceinline__ void set(u4 x, u4 y) {
+    v[0] = unpack_fp8(x[0], x[1]);
+    v[1] = unpack_fp8(x[2], x[3]);
+    v[2] = unpack_fp8(y[0], y[1]);
+    v[3] = unpack_fp8(y[2], y[3]);
+  }
+};
+__device__ __forceinline__ f4 block_sum(const Frag<false> &a, const Frag<false> &b) {
+  return mfma_fp8_16(a.v, b.v, f4{0.f, 0.f, 0.f, 0.f});
+}
+__device__ __forceinline__ f4 block_sum(const Frag<true> &a, const Frag<true> &b) {
+  f4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p = mfma16(a.v[i], b.v[i], p);
+  return p;
 }
 
-// ---- quantization: 16 lanes take one block of 128 of one token, 8 values each
-__global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t grp = id >> 4;
-  if (grp >= a.T * a.G) return;  // 16 lanes at a time, so the shuffles below stay among live lanes
-  const int64_t t = grp / a.G;
-  const int g = (int)(grp - t * a.G), at = g * 128 + 8 * (int)(id & 15);
-  const u4 v = at < a.K ? *(const u4 *)(a.x + t * a.K + at) : u4{0u, 0u, 0u, 0u};
+// ---- quantization: 16 lanes take one block of 128 of one token, 8 values each.
+// The scale's product and the one division per value are the definition's, so that
+// the codes are its codes bit for bit (many quotients of BF16 values lie midway
+// between two codes).
+__device__ __forceinline__ u2 quantize8(u4 v, float *scale) {
   float m = absmax_bf16x8(v, 0.f);
 #pragma unroll
   for (int s = 1; s < 16; s *= 2) m = fmaxf(m, __shfl_xor(m, s, 64));
@@ -69,17 +83,56 @@ __global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
     f[2 * i] = bf16_to_f32(v[i] & 0xFFFFu);
     f[2 * i + 1] = bf16_to_f32(v[i] >> 16);
   }
-  *(u2 *)(a.codes + t * (a.G * (int64_t)128) + at) =
-      u2{e4m3x4(f[0], f[1], f[2], f[3], s), e4m3x4(f[4], f[5], f[6], f[7], s)};
+  *scale = s;
+  return u2{e4m3x4(f[0], f[1], f[2], f[3], s), e4m3x4(f[4], f[5], f[6], f[7], s)};
+}
+
+__global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t grp = id >> 4;
+  if (grp >= a.T * a.G) return;  // 16 lanes at a time, so the shuffles stay among live lanes
+  const int64_t t = grp / a.G;
+  const int g = (int)(grp - t * a.G), at = g * 128 + 8 * (int)(id & 15);
+  float s;
+  const u2 c = quantize8(at < a.K ? *(const u4 *)(a.x + t * a.K + at) : u4{0u, 0u, 0u, 0u}, &s);
+  *(u2 *)(a.codes + t * (a.G * (int64_t)128) + at) = c;
   if ((id & 15) == 0) a.sa[g * a.T + t] = s;
 }
 
-// out[t, n .. n + 4) = round(y + residual)
-__device__ __forceinline__ void store4(const LinearArgs &a, int64_t t, int n, const float *y) {
+// out[t, n .. n + W) = round(y + residual); fast: all W there and rows 16-byte aligned
+template <int W>
+__device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, const float *y, bool fast) {
   const int64_t at = t * a.N + n;
+  if (fast) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= a.N) break;
+    for (int w = 0; w < W; w += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = y[w + i];
+      if (a.residual) {
+        const u4 r = *(const u4_a2 *)(a.residual + at + w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] += bf16_to_f32(r[i] & 0xFFFFu);
+          v[2 * i + 1] += bf16_to_f32(r[i] >> 16);
+        }
+      }
+      if (a.out_bf16) {
+        u4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = (uint32_t)f32_to_bf16_rne(v[2 * i]) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1]) << 16);
+        *(u4 *)((uint16_t *)a.out + at + w) = o;
+      } else {
+        *(f4 *)((float *)a.out + at + w) = f4{v[0], v[1], v[2], v[3]};
+        *(f4 *)((float *)a.out + at + w + 4) = f4{v[4], v[5], v[6], v[7]};
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (n + i >= a.N) continue;
     float v = y[i];
     if (a.residual) v += bf16_to_f32(a.residual[at + i]);
     if (a.out_bf16)
@@ -89,52 +142,320 @@ __device__ __forceinline__ void store4(const LinearArgs &a, int64_t t, int n, co
   }
 }
 
-// ---- the product: a workgroup of 4 waves takes 16 weight rows and 16 tokens,
-// each wave every fourth block of K; operands straight from memory to registers.
-template <bool kExact>
-__global__ __launch_bounds__(256) void linear_stream_kernel(LinearArgs a) {
-  __shared__ float part[4][64][4];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, q = lane >> 4;
+// ---- few and some tokens: a workgroup of W waves takes 16 weight rows and MT
+// times 16 tokens, each wave every W-th block of K; the weights go straight from
+// memory to registers.  kFused: the workgroup quantizes its (at most 16) tokens'
+// rows into LDS while its first weights are on their way; else the codes are read
+// from the workspace.
+constexpr int kStreamWaves = 8;
+// Blocks of 128 that a workgroup quantizes itself at most.
+constexpr int kFusedBlocks = 128;
+
+template <bool kExact, int MT, bool kFused>
+__global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
+  constexpr int W = kStreamWaves, N = 64 * W;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part[W][MT][64][4];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int tiles = (a.N + 15) / 16;
-  const int64_t tt = blockIdx.x / tiles;
-  const int n0 = (int)(blockIdx.x - tt * tiles) * 16;
-  const int64_t t = tt * 16 + r, tc = t < a.T ? t : a.T - 1;
+  const int tt = blockIdx.x / tiles, n0 = (blockIdx.x - tt * tiles) * 16;
+  const int64_t t0 = (int64_t)tt * 16 * MT;
+  const int G = a.G;
+  const int64_t Kp = G * (int64_t)128;
   const int n = n0 + r < a.N ? n0 + r : a.N - 1;   // rows past the end: any row, never stored
-  const uint8_t *wp = a.w + (int64_t)n * a.K, *xp = a.codes + tc * (a.G * (int64_t)128);
-  const float *sw = a.scale + (int64_t)(n0 / 128) * a.G;
-  f4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int g = wave; g < a.G; g += 4) {
+  const uint8_t *wp = a.w + (int64_t)n * a.K;
+  const float *sw = a.scale + (int64_t)(n0 / 128) * G;
+  // chunks past K: the codes are 0 there, so any chunk of the same weight row will do
+  auto weights = [&](int g, u4 &w0, u4 &w1) {
     const int k0 = g * 128 + 16 * q, k1 = k0 + 64;
-    // chunks past K: the codes are 0 there, so any chunk of the same weight row will do
-    const u4 w0 = *(const u4 *)(wp + (k0 < a.K ? k0 : 0)), w1 = *(const u4 *)(wp + (k1 < a.K ? k1 : 0));
-    const u4 x0 = *(const u4 *)(xp + k0), x1 = *(const u4 *)(xp + k1);
-    const f4 p = block_sum<kExact>(w0, w1, x0, x1);
-    const float s = a.sa[g * a.T + tc] * sw[g];
+    w0 = *(const u4 *)(wp + (k0 < a.K ? k0 : 0));
+    w1 = *(const u4 *)(wp + (k1 < a.K ? k1 : 0));
+  };
+  u4 w0, w1;
+  int g = wave;
+  if (g < G) weights(g, w0, w1);
+  const unsigned char *xs = smem;                                   // fused: codes [T][Kp + 16]
+  const float *ss = (const float *)(smem + a.T * (Kp + 16));        // and scales [T][G]
+  if constexpr (kFused) {
+    const int chunks = (int)a.T * G * 16;
+    for (int id = tid; id < chunks; id += N) {                      // multiples of 16: see the shuffles
+      const int t = id / (G * 16), at = (id - t * G * 16) * 8;
+      float s;
+      const u2 c = quantize8(at < a.K ? *(const u4 *)(a.x + (int64_t)t * a.K + at) : u4{0u, 0u, 0u, 0u}, &s);
+      *(u2 *)(smem + t * (Kp + 16) + at) = c;
+      if ((id & 15) == 0) ((float *)ss)[t * G + at / 128] = s;
+    }
+    __syncthreads();
+  }
+  int64_t tc[MT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(p[i], s, acc[i]);
+  for (int m = 0; m < MT; ++m) tc[m] = min(t0 + 16 * m + r, a.T - 1);  // tokens past the end: never stored
+  f4 acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = f4{0.f, 0.f, 0.f, 0.f};
+  while (g < G) {
+    Frag<kExact> w;
+    const u4 c0 = w0, c1 = w1;
+    const int gn = g + W;
+    u4 x[MT][2];
+    float s[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if constexpr (kFused) {
+        const unsigned char *p = xs + tc[m] * (Kp + 16) + g * 128 + 16 * q;
+        x[m][0] = *(const u4 *)p;
+        x[m][1] = *(const u4 *)(p + 64);
+        s[m] = ss[tc[m] * G + g];
+      } else {
+        const uint8_t *p = a.codes + tc[m] * Kp + g * 128 + 16 * q;
+        x[m][0] = *(const u4 *)p;
+        x[m][1] = *(const u4 *)(p + 64);
+        s[m] = a.sa[g * a.T + tc[m]];
+      }
+    }
+    const float f = sw[g];
+    if (gn < G) weights(gn, w0, w1);
+    w.set(c0, c1);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      Frag<kExact> b;
+      b.set(x[m][0], x[m][1]);
+      const f4 p = block_sum(w, b);
+      const float sf = s[m] * f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = __builtin_fmaf(p[i], sf, acc[m][i]);
+    }
+    g = gn;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) part[wave][lane][i] = acc[i];
+  for (int m = 0; m < MT; ++m) *(f4 *)part[wave][m][lane] = acc[m];
   __syncthreads();
-  if (wave == 0 && t < a.T) {
-    float y[4];
+  // wave m adds up token tile m
+  if (wave < MT) {
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = (part[0][lane][i] + part[1][lane][i]) + (part[2][lane][i] + part[3][lane][i]);
-    store4(a, t, n0 + 4 * q, y);
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] += part[w][wave][lane][i];
+    const int64_t t = t0 + 16 * wave + r;
+    if (t < a.T) store<4>(a, t, n0 + 4 * q, y, false);
+  }
+}
+
+// ---- many tokens: tiles of BM tokens x BN weight rows, WM x WN waves, each with
+// TM x 4 results of 16 x 16.
+//
+// A k step is one block of 128: BM rows of activation codes, BN of weight codes (128
+// bytes each) and BM activation scales, copied from global memory straight into
+// one of kStages stages of LDS, kStages - 1 steps ahead; one barrier a step.
+//
+// A wave's 64 weight rows are dealt to its 4 results so that a lane ends up with 16
+// consecutive ones: row rho of result j is weight row 16 (rho / 4) + 4 j + rho % 4, so
+// lane group g (rho / 4 in the result's rows) holds rows 16 g + 4 j + i.  A lane then
+// stores 32 bytes of a token's row and four lanes a line of 128.
+//
+// LDS: chunk c (16 bytes) of row r lies at slot 8 r + (c ^ swz(r)); the 16 rows that
+// 16 lanes read at once are consecutive for the tokens (swz = r / 2) and rho's above
+// for the weights (swz = 2 (r / 16) + r / 2 % 2), 16 different of 2 x 8 slots either way.
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void dma16(const void *g, unsigned char *lds) {
+  __builtin_amdgcn_global_load_lds(g, (lds_void *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(const void *g, unsigned char *lds) {
+  __builtin_amdgcn_global_load_lds(g, (lds_void *)lds, 4, 0, 0);
+}
+// s_waitcnt vmcnt(n), other counters left alone
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+template <int WM, int WN, int TM, int STAGES>
+struct Tile {
+  static constexpr int kWaves = WM * WN, BM = WM * TM * 16, BN = WN * 64;
+  static constexpr int kStages = STAGES;
+  static constexpr int kRowCopies = (BM + BN) / 8 / kWaves;        // per wave and step, 1 KB each
+  static_assert((BM + BN) % (8 * kWaves) == 0, "waves copy whole groups of 8 rows");
+  static constexpr int kScaleRows = BM < 64 ? 64 : BM;             // copied 64 at a time
+  static constexpr int kStageBytes = (BM + BN) * 128 + kScaleRows * 4;
+  static constexpr int kBlocks = (BN + 127) / 128;                 // weight blocks that a tile may touch
+  static constexpr int lds(int G) { return kStages * kStageBytes + kBlocks * G * 4; }
+};
+
+template <bool kExact, int WM, int WN, int TM, int STAGES>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void linear_tiles_kernel(LinearArgs a) {
+  using L = Tile<WM, WN, TM, STAGES>;
+  constexpr int BM = L::BM, BN = L::BN, kStages = L::kStages, NC = L::kRowCopies;
+  extern __shared__ __align__(16) unsigned char smem[];
+  float *sws = (float *)(smem + kStages * L::kStageBytes);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int G = a.G, K = a.K;
+  const int64_t Kp = G * (int64_t)128;
+  // ---- tile of this workgroup.  The 8 XCDs take contiguous ranges; inside a range
+  // tiles go down kDown token tiles before the next column of weight rows, so that
+  // the tiles at work at one time share rows of both kinds in their XCD's cache.
+  constexpr int kDown = 8;
+  const int mt = (int)((a.T + BM - 1) / BM), nt = (a.N + BN - 1) / BN, all = mt * nt;
+  const int per = (all + 7) / 8, x = blockIdx.x & 7, s0 = blockIdx.x >> 3;
+  const int id = x * per + s0;
+  if (s0 >= per || id >= all) return;
+  const int band = id / (kDown * nt), first = band * kDown, high = min(kDown, mt - first), in = id - band * kDown * nt;
+  const int64_t t0 = (int64_t)(first + in % high) * BM;
+  const int n0 = in / high * BN;
+  // ---- weight scales of the tile's blocks (0 past the end)
+  const int nb = (a.N + 127) / 128;
+  for (int i = tid; i < L::kBlocks * G; i += 64 * L::kWaves) {
+    const int b = i / G, g = i - b * G, at = n0 / 128 + b;
+    sws[i] = at < nb ? a.scale[(int64_t)at * G + g] : 0.f;
+  }
+  // ---- copies: number p of this wave fills rows 8 (NC wave + p) + [0, 8) of the
+  // stage, tokens first; rows past the end copy the last row, which is never stored
+  const uint8_t *xbase = a.codes + t0 * Kp, *wbase = a.w + (int64_t)n0 * K;
+  uint32_t off[NC];
+  bool token[NC];
+  int chunk[NC];
+#pragma unroll
+  for (int p = 0; p < NC; ++p) {
+    const int row = 8 * (NC * wave + p) + (lane >> 3);
+    token[p] = 8 * (NC * wave + p) < BM;
+    if (token[p]) {
+      chunk[p] = (lane & 7) ^ ((row >> 1) & 7);
+      off[p] = (uint32_t)(min((int64_t)row, a.T - 1 - t0) * Kp) + 16 * chunk[p];
+    } else {
+      const int n = row - BM;
+      chunk[p] = (lane & 7) ^ (2 * ((n >> 4) & 3) + ((n >> 1) & 1));
+      off[p] = (uint32_t)min(n, a.N - 1 - n0) * (uint32_t)K;
+    }
+  }
+  // activation scales: wave w copies those of tokens 64 (w % (kScaleRows / 64)) + [0, 64)
+  const int sg = wave % (L::kScaleRows / 64);
+  const float *sbase = a.sa + min(t0 + 64 * sg + lane, a.T - 1);
+  auto issue = [&](int g) {
+    unsigned char *st = smem + (g % kStages) * L::kStageBytes;
+#pragma unroll
+    for (int p = 0; p < NC; ++p) {
+      const uint8_t *src;
+      if (token[p]) {
+        src = xbase + g * 128 + off[p];
+      } else {
+        // chunks past K meet codes of 0: any chunk of the same row will do
+        const int k = g * 128 + 16 * chunk[p];
+        src = wbase + off[p] + (k < K ? k : 0);
+      }
+      dma16(src, st + 1024 * (NC * wave + p));
+    }
+    dma4(sbase + (int64_t)g * a.T, st + (BM + BN) * 128 + 256 * sg);
+  };
+  // ---- the wave's part of the tile
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int tok = wm * TM * 16 + r;                                   // + 16 m
+  const int wrow = wn * 64 + 16 * (r >> 2) + (r & 3);                 // + 4 j
+  const int blk = (wn * 64) / 128;
+  f4 acc[TM][4];
+#pragma unroll
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[m][j] = f4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](int g) {
+    const unsigned char *st = smem + (g % kStages) * L::kStageBytes, *ws = st + BM * 128;
+    const float *ss = (const float *)(st + (BM + BN) * 128);
+    const float f = sws[blk * G + g];
+    Frag<kExact> w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = wrow + 4 * j, z = 2 * ((n >> 4) & 3) + ((n >> 1) & 1);
+      w[j].set(*(const u4 *)(ws + n * 128 + 16 * (q ^ z)), *(const u4 *)(ws + n * 128 + 16 * ((q + 4) ^ z)));
+    }
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const int t = tok + 16 * m, z = (t >> 1) & 7;
+      Frag<kExact> b;
+      b.set(*(const u4 *)(st + t * 128 + 16 * (q ^ z)), *(const u4 *)(st + t * 128 + 16 * ((q + 4) ^ z)));
+      const float s = ss[t] * f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f4 p = block_sum(w[j], b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][j][i] = __builtin_fmaf(p[i], s, acc[m][j][i]);
+      }
+    }
+  };
+  __syncthreads();   // the weight scales; nothing else is in flight yet
+  for (int g = 0; g < kStages - 1 && g < G; ++g) issue(g);
+  for (int g = 0; g < G; ++g) {
+    // step g's copies have landed (later ones stay in flight), for every wave; and
+    // every wave is done with step g - 1, whose stage the next copies fill
+    if (kStages > 2 && g + 1 < G)
+      wait_vm<(kStages - 2) * (NC + 1)>();
+    else
+      wait_vm<0>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (g + kStages - 1 < G) issue(g + kStages - 1);
+    compute(g);
+  }
+  // ---- results: token tok + 16 m, weight rows 64 wn + 16 q + [0, 16)
+  const int n = n0 + wn * 64 + 16 * q;
+  if (n >= a.N) return;
+  const bool fast = n + 16 <= a.N && a.N % 8 == 0 && ((uintptr_t)a.out & 15) == 0;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int64_t t = t0 + tok + 16 * m;
+    if (t >= a.T) continue;
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[4 * j + i] = acc[m][j][i];
+    store<16>(a, t, n, y, fast);
+  }
+}
+
+template <bool kExact, int WM, int WN, int TM, int STAGES>
+hipError_t run_tiles(const LinearArgs &a, hipStream_t s) {
+  using L = Tile<WM, WN, TM, STAGES>;
+  const int64_t all = ((a.T + L::BM - 1) / L::BM) * ((a.N + L::BN - 1) / L::BN);
+  if (all > 0x7FFFFFF0) return hipErrorInvalidConfiguration;
+  raise_lds_limit((const void *)linear_tiles_kernel<kExact, WM, WN, TM, STAGES>);
+  linear_tiles_kernel<kExact, WM, WN, TM, STAGES>
+      <<<dim3((unsigned)((all + 7) / 8 * 8)), dim3(64 * L::kWaves), L::lds(a.G), s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool kExact, int MT, bool kFused>
+hipError_t run_stream(const LinearArgs &a, hipStream_t s) {
+  const int64_t wgs = (int64_t)((a.N + 15) / 16) * ((a.T + 16 * MT - 1) / (16 * MT));
+  if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const size_t lds = kFused ? a.T * (a.G * (size_t)128 + 16 + a.G * 4) : 0;
+  linear_stream_kernel<kExact, MT, kFused><<<dim3((unsigned)wgs), dim3(64 * kStreamWaves), lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool kExact>
+hipError_t run_linear(const LinearArgs &a, hipStream_t s) {
+  if (a.T <= 16 && a.T * a.G <= kFusedBlocks) return run_stream<kExact, 1, true>(a, s);
+  const int64_t quant = (a.T * a.G * 16 + 255) / 256;
+  if (quant > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  linear_quant_kernel<<<dim3((unsigned)quant), dim3(256), 0, s>>>(a);
+  if (a.T <= 16) return run_stream<kExact, 1, false>(a, s);
+  if (a.T <= 32) return run_stream<kExact, 2, false>(a, s);
+  if (a.T <= 64) return run_stream<kExact, 4, false>(a, s);
+  if constexpr (kExact) {
+    return run_tiles<true, 2, 2, 2, 3>(a, s);
+  } else {
+    const int64_t big = ((a.T + 255) / 256) * ((a.N + 255) / 256);
+    if (big >= 192) return run_tiles<false, 2, 4, 8, 2>(a, s);
+    return run_tiles<false, 2, 2, 2, 3>(a, s);
   }
 }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs &a, hipStream_t s) {
-  const int64_t quant = (a.T * a.G * 16 + 255) / 256, tiles = (int64_t)((a.N + 15) / 16) * ((a.T + 15) / 16);
-  if (quant > 0x7FFFFFFF || tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  linear_quant_kernel<<<dim3((unsigned)quant), dim3(256), 0, s>>>(a);
-  if (a.out_bf16)
-    linear_stream_kernel<false><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(a);
-  else
-    linear_stream_kernel<true><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+  return a.out_bf16 ? run_linear<false>(a, s) : run_linear<true>(a, s);
 }
 
 }  // namespace mq
