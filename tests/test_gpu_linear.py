@@ -89,6 +89,43 @@ def test_sizes(t, n, k, dtype):
     check(t, n, k, dtype, residual=(t + n) % 2 == 0, seed=t + 1)
 
 
+@pytest.mark.parametrize("t,n,k", [(10, 4999, 2064), (16, 4900, 1040), (20, 4999, 400), (33, 5000, 272), (64, 4801, 2064),
+                                   (130, 1700, 400), (200, 2400, 144),      # streamed, 32 weight rows a workgroup
+                                   (70, 7000, 144), (333, 2000, 400),       # tiles of 64 x 64
+                                   (2049, 2100, 272),                       # tiles of 64 x 128
+                                   (2050, 2570, 144)])                      # tiles of 128 x 128
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_each_way(t, n, k, dtype):
+    check(t, n, k, dtype, residual=n % 2 == 0, seed=t)
+
+
+@pytest.mark.parametrize("n", [8200, 8201])
+def test_the_largest_tiles(n):
+    """256 x 256; the reference in 64 bits on the GPU, a block's largest product bounded
+    by its factors' largest."""
+    t, k = 8197, 272
+    w, s = make(n, k, 1)
+    x = rows(t, k, 1)
+    r = torch.randn(t, n, device="cuda").to(BF)
+    out = torch.full((t + 1, n), 7.0, dtype=BF, device="cuda")
+    Linear(w, s).forward(x, residual=r, out=out[:t])
+    codes, sa = olin.quantize_rows(f64(x))
+    a = torch.from_numpy(codecs.decode_e4m3(codes) * np.repeat(sa.astype(np.float64), 128, 1))[:, :k].cuda()
+    v = torch.from_numpy(codecs.decode_e4m3(w.cpu().numpy())).cuda()
+    v = v * s.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    y, size, largest = r.double(), r.double().abs(), torch.zeros(t, n, dtype=torch.float64, device="cuda")
+    for at in range(0, k, 128):
+        p, q = a[:, at:at + 128], v[:, at:at + 128]
+        y, size = y + p @ q.t(), size + p.abs() @ q.abs().t()
+        largest += p.abs().amax(1)[:, None] * q.abs().amax(1)
+    assert torch.all(out[t] == 7.0)
+    off = (out[:t].double() - y).abs()
+    c = (128 * 2.0 ** -23 + 27 * 2.0 ** -24) * size + 2.0 ** -9 * largest
+    assert bool((off <= c + 2.0 ** -8 * (y.abs() + c)).all())
+    near = 2.0 ** -8 / 3 ** 0.5 * float(y.norm()) + (128 / 3) ** 0.5 * 2.0 ** -16 * float(largest.norm())
+    assert float(off.norm()) <= 1.2 * near
+
+
 @pytest.mark.parametrize("t", [1, 2, 3, 4, 5, 7, 8, 9, 12, 16, 20, 24, 31, 32, 40, 48, 63, 80, 96, 127, 160, 192])
 def test_few_tokens(t):
     for n, k in ((512, 2048), (2048, 512), (300, 1552)):

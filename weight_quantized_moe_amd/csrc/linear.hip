@@ -35,7 +35,7 @@ typedef u4 u4_a2 __attribute__((aligned(2)));
 // as long as both agree); of the result, token l % 16 and weight rows
 // 4 (l / 16) + [0, 4).
 __device__ __forceinline__ f4 mfma_fp8_16(const i8v &a, const i8v &b, const f4 &c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 // A lane's 32 codes of a row and a block of 128, as its products take them.
@@ -71,7 +71,11 @@ __device__ __forceinline__ f4 block_sum(const Frag<true> &a, const Frag<true> &b
 // ---- quantization: 16 lanes take one block of 128 of one token, 8 values each.
 // The scale's product and the one division per value are the definition's, so that
 // the codes are its codes bit for bit (many quotients of BF16 values lie midway
-// between two codes).
+// between two codes).  The division v / s by one reciprocal per block: with y the
+// rounded 1 / s and q the rounded v y, which is within a step of v / s, the
+// remainder v - q s is exact in one FMA and q + remainder y rounds to the rounded
+// v / s (Markstein's theorem), unless the remainder underflows or the mantissa of s
+// is all ones: such blocks, rare ones, divide.
 __device__ __forceinline__ u2 quantize8(u4 v, float *scale) {
   float m = absmax_bf16x8(v, 0.f);
 #pragma unroll
@@ -84,7 +88,21 @@ __device__ __forceinline__ u2 quantize8(u4 v, float *scale) {
     f[2 * i + 1] = bf16_to_f32(v[i] >> 16);
   }
   *scale = s;
-  return u2{e4m3x4(f[0], f[1], f[2], f[3], s), e4m3x4(f[4], f[5], f[6], f[7], s)};
+  if (__any(!(s >= 0x1p-60f && s <= 0x1p120f) || (__float_as_uint(s) & 0x7FFFFFu) == 0x7FFFFFu))
+    return u2{e4m3x4(f[0], f[1], f[2], f[3], s), e4m3x4(f[4], f[5], f[6], f[7], s)};
+  const float y = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = f[i] * y;
+    f[i] = __builtin_amdgcn_fmed3f(__builtin_fmaf(__builtin_fmaf(-q, s, f[i]), y, q), -448.f, 448.f);
+  }
+  u2 c;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], 0, false);
+    c[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], w, true);
+  }
+  return c;
 }
 
 __global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
@@ -103,9 +121,9 @@ __global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
 template <int W>
 __device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, const float *y, bool fast) {
   const int64_t at = t * a.N + n;
-  if (fast) {
+  if (W >= 8 && fast) {
 #pragma unroll
-    for (int w = 0; w < W; w += 8) {
+    for (int w = 0; w + 8 <= W; w += 8) {
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = y[w + i];
@@ -142,40 +160,53 @@ __device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, con
   }
 }
 
-// ---- few and some tokens: a workgroup of W waves takes 16 weight rows and MT
-// times 16 tokens, each wave every W-th block of K; the weights go straight from
-// memory to registers.  kFused: the workgroup quantizes its (at most 16) tokens'
-// rows into LDS while its first weights are on their way; else the codes are read
-// from the workspace.
+// ---- few and some tokens: a workgroup of 8 waves takes 16 NT weight rows and 16 MT
+// tokens, each wave every 8th block of K, U of its blocks at a time, whose loads are
+// all on their way before the first product; the weights go straight from memory to
+// registers.  kFused: the workgroup quantizes its (at most 16) tokens' rows into LDS
+// while its first weights are on their way; else the codes are read from the
+// workspace.
 constexpr int kStreamWaves = 8;
 // Blocks of 128 that a workgroup quantizes itself at most.
 constexpr int kFusedBlocks = 128;
+// Fewest workgroups for a larger part of the result to each, and most of them for
+// which the axis K over the waves of a workgroup still beats tiles in LDS.
+constexpr int64_t kStreamLeast = 150, kStreamMost = 256;
 
-template <bool kExact, int MT, bool kFused>
+template <bool kExact, int NT, int MT, int U, bool kFused>
 __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
   constexpr int W = kStreamWaves, N = 64 * W;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float part[W][MT][64][4];
+  __shared__ f4 part[W][NT * MT][64];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, q = lane >> 4;
-  const int tiles = (a.N + 15) / 16;
-  const int tt = blockIdx.x / tiles, n0 = (blockIdx.x - tt * tiles) * 16;
+  const int tiles = (a.N + 16 * NT - 1) / (16 * NT);
+  const int tt = blockIdx.x / tiles, n0 = (blockIdx.x - tt * tiles) * 16 * NT;
   const int64_t t0 = (int64_t)tt * 16 * MT;
   const int G = a.G;
   const int64_t Kp = G * (int64_t)128;
-  const int n = n0 + r < a.N ? n0 + r : a.N - 1;   // rows past the end: any row, never stored
-  const uint8_t *wp = a.w + (int64_t)n * a.K;
+  const uint8_t *wp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) wp[j] = a.w + (int64_t)min(n0 + 16 * j + r, a.N - 1) * a.K;  // rows past the end: never stored
   const float *sw = a.scale + (int64_t)(n0 / 128) * G;
-  // chunks past K: the codes are 0 there, so any chunk of the same weight row will do
-  auto weights = [&](int g, u4 &w0, u4 &w1) {
-    const int k0 = g * 128 + 16 * q, k1 = k0 + 64;
-    w0 = *(const u4 *)(wp + (k0 < a.K ? k0 : 0));
-    w1 = *(const u4 *)(wp + (k1 < a.K ? k1 : 0));
+  u4 w[U][NT][2];
+  float f[U];
+  // blocks g, g + W, ...; those past the last are the last once more, times 0
+  auto weights = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = min(g + u * W, G - 1), k0 = at * 128 + 16 * q, k1 = k0 + 64;
+      f[u] = g + u * W < G ? sw[at] : 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        // chunks past K: the codes are 0 there, so any chunk of the same weight row will do
+        w[u][j][0] = *(const u4 *)(wp[j] + (k0 < a.K ? k0 : 0));
+        w[u][j][1] = *(const u4 *)(wp[j] + (k1 < a.K ? k1 : 0));
+      }
+    }
   };
-  u4 w0, w1;
-  int g = wave;
-  if (g < G) weights(g, w0, w1);
+  weights(wave);
   const unsigned char *xs = smem;                                   // fused: codes [T][Kp + 16]
-  const float *ss = (const float *)(smem + a.T * (Kp + 16));        // and scales [T][G]
+  float *ss = (float *)(smem + a.T * (Kp + 16));                    // and scales [T][G]
   if constexpr (kFused) {
     const int chunks = (int)a.T * G * 16;
     for (int id = tid; id < chunks; id += N) {                      // multiples of 16: see the shuffles
@@ -183,62 +214,68 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
       float s;
       const u2 c = quantize8(at < a.K ? *(const u4 *)(a.x + (int64_t)t * a.K + at) : u4{0u, 0u, 0u, 0u}, &s);
       *(u2 *)(smem + t * (Kp + 16) + at) = c;
-      if ((id & 15) == 0) ((float *)ss)[t * G + at / 128] = s;
+      if ((id & 15) == 0) ss[t * G + at / 128] = s;
     }
     __syncthreads();
   }
   int64_t tc[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) tc[m] = min(t0 + 16 * m + r, a.T - 1);  // tokens past the end: never stored
-  f4 acc[MT];
+  f4 acc[NT][MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f4{0.f, 0.f, 0.f, 0.f};
-  while (g < G) {
-    Frag<kExact> w;
-    const u4 c0 = w0, c1 = w1;
-    const int gn = g + W;
-    u4 x[MT][2];
-    float s[MT];
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if constexpr (kFused) {
-        const unsigned char *p = xs + tc[m] * (Kp + 16) + g * 128 + 16 * q;
-        x[m][0] = *(const u4 *)p;
-        x[m][1] = *(const u4 *)(p + 64);
-        s[m] = ss[tc[m] * G + g];
-      } else {
-        const uint8_t *p = a.codes + tc[m] * Kp + g * 128 + 16 * q;
-        x[m][0] = *(const u4 *)p;
-        x[m][1] = *(const u4 *)(p + 64);
-        s[m] = a.sa[g * a.T + tc[m]];
+    for (int m = 0; m < MT; ++m) acc[j][m] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int g = wave; g < G; g += U * W) {
+    if (g != wave) weights(g);
+    u4 x[U][MT][2];
+    float s[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = min(g + u * W, G - 1);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint8_t *p = kFused ? xs + tc[m] * (Kp + 16) : a.codes + tc[m] * Kp;
+        x[u][m][0] = *(const u4 *)(p + at * 128 + 16 * q);
+        x[u][m][1] = *(const u4 *)(p + at * 128 + 16 * q + 64);
+        s[u][m] = kFused ? ss[tc[m] * G + at] : a.sa[at * a.T + tc[m]];
       }
     }
-    const float f = sw[g];
-    if (gn < G) weights(gn, w0, w1);
-    w.set(c0, c1);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      Frag<kExact> b;
-      b.set(x[m][0], x[m][1]);
-      const f4 p = block_sum(w, b);
-      const float sf = s[m] * f;
+    for (int u = 0; u < U; ++u) {
+      Frag<kExact> wf[NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][i] = __builtin_fmaf(p[i], sf, acc[m][i]);
+      for (int j = 0; j < NT; ++j) wf[j].set(w[u][j][0], w[u][j][1]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        Frag<kExact> b;
+        b.set(x[u][m][0], x[u][m][1]);
+        const float sf = s[u][m] * f[u];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const f4 p = block_sum(wf[j], b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][m][i] = __builtin_fmaf(p[i], sf, acc[j][m][i]);
+        }
+      }
     }
-    g = gn;
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) *(f4 *)part[wave][m][lane] = acc[m];
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) part[wave][j * MT + m][lane] = acc[j][m];
   __syncthreads();
-  // wave m adds up token tile m
-  if (wave < MT) {
+  // a wave adds up a result of 16 x 16
+  if (wave < NT * MT) {
     float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < W; ++w)
+    for (int v = 0; v < W; ++v) {
+      const f4 p = part[v][wave][lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += part[w][wave][lane][i];
-    const int64_t t = t0 + 16 * wave + r;
-    if (t < a.T) store<4>(a, t, n0 + 4 * q, y, false);
+      for (int i = 0; i < 4; ++i) y[i] += p[i];
+    }
+    const int64_t t = t0 + 16 * (wave % MT) + r;
+    if (t < a.T) store<4>(a, t, n0 + 16 * (wave / MT) + 4 * q, y, false);
   }
 }
 
@@ -275,8 +312,8 @@ template <int WM, int WN, int TM, int STAGES>
 struct Tile {
   static constexpr int kWaves = WM * WN, BM = WM * TM * 16, BN = WN * 64;
   static constexpr int kStages = STAGES;
-  static constexpr int kRowCopies = (BM + BN) / 8 / kWaves;        // per wave and step, 1 KB each
-  static_assert((BM + BN) % (8 * kWaves) == 0, "waves copy whole groups of 8 rows");
+  static constexpr int kTokenCopies = BM / 8 / kWaves, kWeightCopies = BN / 8 / kWaves;  // per wave and step, 1 KB each
+  static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "waves copy whole groups of 8 rows");
   static constexpr int kScaleRows = BM < 64 ? 64 : BM;             // copied 64 at a time
   static constexpr int kStageBytes = (BM + BN) * 128 + kScaleRows * 4;
   static constexpr int kBlocks = (BN + 127) / 128;                 // weight blocks that a tile may touch
@@ -287,7 +324,7 @@ template <bool kExact, int WM, int WN, int TM, int STAGES>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void linear_tiles_kernel(LinearArgs a) {
   using L = Tile<WM, WN, TM, STAGES>;
-  constexpr int BM = L::BM, BN = L::BN, kStages = L::kStages, NC = L::kRowCopies;
+  constexpr int BM = L::BM, BN = L::BN, kStages = L::kStages, CX = L::kTokenCopies, CW = L::kWeightCopies;
   extern __shared__ __align__(16) unsigned char smem[];
   float *sws = (float *)(smem + kStages * L::kStageBytes);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, q = lane >> 4;
@@ -310,41 +347,42 @@ void linear_tiles_kernel(LinearArgs a) {
     const int b = i / G, g = i - b * G, at = n0 / 128 + b;
     sws[i] = at < nb ? a.scale[(int64_t)at * G + g] : 0.f;
   }
-  // ---- copies: number p of this wave fills rows 8 (NC wave + p) + [0, 8) of the
-  // stage, tokens first; rows past the end copy the last row, which is never stored
+  // ---- copies: a wave's number p fills rows 8 (CX wave + p) + [0, 8) of the tokens'
+  // part of the stage, CW of the weights'; rows past the end copy the last row,
+  // which is never stored
   const uint8_t *xbase = a.codes + t0 * Kp, *wbase = a.w + (int64_t)n0 * K;
-  uint32_t off[NC];
-  bool token[NC];
-  int chunk[NC];
+  uint32_t xoff[CX], woff[CW];
 #pragma unroll
-  for (int p = 0; p < NC; ++p) {
-    const int row = 8 * (NC * wave + p) + (lane >> 3);
-    token[p] = 8 * (NC * wave + p) < BM;
-    if (token[p]) {
-      chunk[p] = (lane & 7) ^ ((row >> 1) & 7);
-      off[p] = (uint32_t)(min((int64_t)row, a.T - 1 - t0) * Kp) + 16 * chunk[p];
-    } else {
-      const int n = row - BM;
-      chunk[p] = (lane & 7) ^ (2 * ((n >> 4) & 3) + ((n >> 1) & 1));
-      off[p] = (uint32_t)min(n, a.N - 1 - n0) * (uint32_t)K;
-    }
+  for (int p = 0; p < CX; ++p) {
+    const int row = 8 * (CX * wave + p) + (lane >> 3);
+    xoff[p] = (uint32_t)(min((int64_t)row, a.T - 1 - t0) * Kp) + 16 * ((lane & 7) ^ ((row >> 1) & 7));
   }
+  auto wchunk = [&](int p) {
+    const int row = 8 * (CW * wave + p) + (lane >> 3);
+    return 16 * ((lane & 7) ^ (2 * ((row >> 4) & 3) + ((row >> 1) & 1)));
+  };
+#pragma unroll
+  for (int p = 0; p < CW; ++p)
+    woff[p] = (uint32_t)min(8 * (CW * wave + p) + (lane >> 3), a.N - 1 - n0) * (uint32_t)K + wchunk(p);
   // activation scales: wave w copies those of tokens 64 (w % (kScaleRows / 64)) + [0, 64)
   const int sg = wave % (L::kScaleRows / 64);
   const float *sbase = a.sa + min(t0 + 64 * sg + lane, a.T - 1);
   auto issue = [&](int g) {
     unsigned char *st = smem + (g % kStages) * L::kStageBytes;
+    const uint8_t *xg = xbase + g * 128, *wg = wbase + g * 128;
 #pragma unroll
-    for (int p = 0; p < NC; ++p) {
-      const uint8_t *src;
-      if (token[p]) {
-        src = xbase + g * 128 + off[p];
-      } else {
-        // chunks past K meet codes of 0: any chunk of the same row will do
-        const int k = g * 128 + 16 * chunk[p];
-        src = wbase + off[p] + (k < K ? k : 0);
+    for (int p = 0; p < CX; ++p) dma16(xg + xoff[p], st + 1024 * (CX * wave + p));
+    if (g * 128 + 128 <= K) {
+#pragma unroll
+      for (int p = 0; p < CW; ++p) dma16(wg + woff[p], st + BM * 128 + 1024 * (CW * wave + p));
+    } else {
+      // chunks past K meet codes of 0: the same row's first one will do
+#pragma unroll
+      for (int p = 0; p < CW; ++p) {
+        const int c = wchunk(p);
+        const uint32_t back = g * 128 + c < K ? 0u : (uint32_t)(g * 128 + c);
+        dma16(wg + woff[p] - back, st + BM * 128 + 1024 * (CW * wave + p));
       }
-      dma16(src, st + 1024 * (NC * wave + p));
     }
     dma4(sbase + (int64_t)g * a.T, st + (BM + BN) * 128 + 256 * sg);
   };
@@ -358,28 +396,50 @@ void linear_tiles_kernel(LinearArgs a) {
   for (int m = 0; m < TM; ++m)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[m][j] = f4{0.f, 0.f, 0.f, 0.f};
+  // One k step: the next token rows' operand and the sums of the rows before are in
+  // work while the matrix units multiply (the barriers keep the compiler from
+  // putting each read right in front of its use).
   auto compute = [&](int g) {
     const unsigned char *st = smem + (g % kStages) * L::kStageBytes, *ws = st + BM * 128;
     const float *ss = (const float *)(st + (BM + BN) * 128);
     const float f = sws[blk * G + g];
-    Frag<kExact> w[4];
+    auto token = [&](int m, Frag<kExact> &b) {
+      const int t = tok + 16 * m, z = (t >> 1) & 7;
+      b.set(*(const u4 *)(st + t * 128 + 16 * (q ^ z)), *(const u4 *)(st + t * 128 + 16 * ((q + 4) ^ z)));
+    };
+    Frag<kExact> w[4], b[2];
+    float sa[TM];
+    token(0, b[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = wrow + 4 * j, z = 2 * ((n >> 4) & 3) + ((n >> 1) & 1);
       w[j].set(*(const u4 *)(ws + n * 128 + 16 * (q ^ z)), *(const u4 *)(ws + n * 128 + 16 * ((q + 4) ^ z)));
     }
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      const int t = tok + 16 * m, z = (t >> 1) & 7;
-      Frag<kExact> b;
-      b.set(*(const u4 *)(st + t * 128 + 16 * (q ^ z)), *(const u4 *)(st + t * 128 + 16 * ((q + 4) ^ z)));
-      const float s = ss[t] * f;
+    for (int m = 0; m < TM; ++m) sa[m] = ss[tok + 16 * m] * f;
+    f4 p[2][4];
+#pragma unroll
+    for (int m = 0; m <= TM; ++m) {
+      if (m + 1 < TM) token(m + 1, b[(m + 1) & 1]);
+      if (m < TM) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[m & 1][j] = block_sum(w[j], b[m & 1]);
+      }
+      if (m > 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[m - 1][j][i] = __builtin_fmaf(p[(m - 1) & 1][j][i], sa[m - 1], acc[m - 1][j][i]);
+      }
+      // reads for m + 1, then a product of m and four sums of m - 1 in turn
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f4 p = block_sum(w[j], b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = __builtin_fmaf(p[i], s, acc[m][j][i]);
+        __builtin_amdgcn_sched_group_barrier(0x8, kExact ? 4 : 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   __syncthreads();   // the weight scales; nothing else is in flight yet
@@ -387,8 +447,8 @@ void linear_tiles_kernel(LinearArgs a) {
   for (int g = 0; g < G; ++g) {
     // step g's copies have landed (later ones stay in flight), for every wave; and
     // every wave is done with step g - 1, whose stage the next copies fill
-    if (kStages > 2 && g + 1 < G)
-      wait_vm<(kStages - 2) * (NC + 1)>();
+    if (kStages > 2 && g + kStages - 2 < G)
+      wait_vm<(kStages - 2) * (CX + CW + 1)>();
     else
       wait_vm<0>();
     asm volatile("" ::: "memory");
@@ -425,31 +485,34 @@ hipError_t run_tiles(const LinearArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool kExact, int MT, bool kFused>
+template <bool kExact, int NT, int MT, int U, bool kFused>
 hipError_t run_stream(const LinearArgs &a, hipStream_t s) {
-  const int64_t wgs = (int64_t)((a.N + 15) / 16) * ((a.T + 16 * MT - 1) / (16 * MT));
+  const int64_t wgs = (int64_t)((a.N + 16 * NT - 1) / (16 * NT)) * ((a.T + 16 * MT - 1) / (16 * MT));
   if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const size_t lds = kFused ? a.T * (a.G * (size_t)128 + 16 + a.G * 4) : 0;
-  linear_stream_kernel<kExact, MT, kFused><<<dim3((unsigned)wgs), dim3(64 * kStreamWaves), lds, s>>>(a);
+  linear_stream_kernel<kExact, NT, MT, U, kFused><<<dim3((unsigned)wgs), dim3(64 * kStreamWaves), lds, s>>>(a);
   return hipGetLastError();
 }
 
 template <bool kExact>
 hipError_t run_linear(const LinearArgs &a, hipStream_t s) {
-  if (a.T <= 16 && a.T * a.G <= kFusedBlocks) return run_stream<kExact, 1, true>(a, s);
+  if (a.T <= 16 && a.T * a.G <= kFusedBlocks) return run_stream<kExact, 1, 1, 1, true>(a, s);
   const int64_t quant = (a.T * a.G * 16 + 255) / 256;
   if (quant > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   linear_quant_kernel<<<dim3((unsigned)quant), dim3(256), 0, s>>>(a);
-  if (a.T <= 16) return run_stream<kExact, 1, false>(a, s);
-  if (a.T <= 32) return run_stream<kExact, 2, false>(a, s);
-  if (a.T <= 64) return run_stream<kExact, 4, false>(a, s);
-  if constexpr (kExact) {
-    return run_tiles<true, 2, 2, 2, 3>(a, s);
-  } else {
-    const int64_t big = ((a.T + 255) / 256) * ((a.N + 255) / 256);
-    if (big >= 192) return run_tiles<false, 2, 4, 8, 2>(a, s);
-    return run_tiles<false, 2, 2, 2, 3>(a, s);
+  auto cover = [&](int bm, int bn) { return ((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (a.T <= 64 || cover(64, 32) <= kStreamMost) {
+    if (a.T > 32 && cover(64, 32) >= kStreamLeast) return run_stream<kExact, 2, 4, 2, false>(a, s);
+    if (a.T > 16 && cover(32, 32) >= kStreamLeast) return run_stream<kExact, 2, 2, 2, false>(a, s);
+    if (cover(16, 32) >= kStreamLeast) return run_stream<kExact, 2, 1, 2, false>(a, s);
+    return run_stream<kExact, 1, 1, 2, false>(a, s);
   }
+  if constexpr (!kExact) {
+    if (cover(256, 256) >= 1024) return run_tiles<false, 2, 4, 8, 2>(a, s);
+  }
+  if (cover(128, 128) >= 320) return run_tiles<kExact, 2, 2, 4, 2>(a, s);
+  if (cover(64, 128) >= 512) return run_tiles<kExact, 2, 2, 2, 3>(a, s);
+  return run_tiles<kExact, 4, 1, 1, 4>(a, s);
 }
 
 }  // namespace
