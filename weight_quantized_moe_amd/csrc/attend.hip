@@ -408,9 +408,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_pieces_kernel(AttendArg
 }
 
 // ---- the pieces of a unit joined, a workgroup per query head: 64 pairs of D (or
-// more, in turn) on each of 4 waves, every wave a fourth of the pieces.
+// more, in turn) on each of 4 waves, every wave a fourth of the pieces.  The first
+// pieces' values are asked for together with the maxima and sums.
+constexpr int kGroupsMost = 1024;   // of a plan, so no unit has more pieces
+constexpr int kAhead = 8;
+
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan plan) {
-  __shared__ float sx[4][64], sy[4][64];
+  __shared__ float sx[4][64], sy[4][64], weight[kGroupsMost];
   const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
   const int b = blockIdx.x / units, kt = blockIdx.x - b * units, r = blockIdx.y;
   const int f0 = plan.first[b], k = (plan.first[b + 1] - f0) / units;
@@ -419,24 +423,44 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pla
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = a.D;
   const int64_t size = 32 + 16 * (int64_t)D;
   const float *part = plan.parts + (f0 + kt * k) * size;
+  float2 ahead[kAhead];
+  auto values = [&](int w, int d) { return *(const float2 *)(part + w * size + 32 + r * D + d); };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    ahead[i] = float2{0.f, 0.f};
+    if (wave + 4 * i < k && 2 * lane < D) ahead[i] = values(wave + 4 * i, 2 * lane);
+  }
   float m = -INFINITY, l = 0.f;
   for (int w = lane; w < k; w += 64) m = fmaxf(m, part[w * size + r]);
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
   const float mm = m == -INFINITY ? 0.f : m;
-  for (int w = lane; w < k; w += 64) l += part[w * size + 16 + r] * __builtin_amdgcn_exp2f(part[w * size + r] - mm);
+  for (int w = lane; w < k; w += 64) {
+    const float f = __builtin_amdgcn_exp2f(part[w * size + r] - mm);
+    l += part[w * size + 16 + r] * f;
+    if (wave == 0) weight[w] = f;
+  }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, 64);
+  __syncthreads();
   for (int d0 = 0; d0 < D; d0 += 128) {
     const int d = d0 + 2 * lane;
     float x = 0.f, y = 0.f;
     if (d < D) {
-#pragma unroll 8
-      for (int w = wave; w < k; w += 4) {
-        const float f = __builtin_amdgcn_exp2f(part[w * size + r] - mm);
-        const float2 o = *(const float2 *)(part + w * size + 32 + r * D + d);
-        x += f * o.x;
-        y += f * o.y;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int w = wave + 4 * i;
+        if (w < k) {
+          const float2 o = d0 ? values(w, d) : ahead[i];
+          x += weight[w] * o.x;
+          y += weight[w] * o.y;
+        }
+      }
+#pragma unroll 4
+      for (int w = wave + 4 * kAhead; w < k; w += 4) {
+        const float2 o = values(w, d);
+        x += weight[w] * o.x;
+        y += weight[w] * o.y;
       }
     }
     __syncthreads();
@@ -454,7 +478,6 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pla
 // smaller pieces so that the last ones end together (512 - units against 1024 -
 // units groups: 16 units of 3100 to 4096 tiles 98 and 110 us; 192 units of 1 to 256
 // tiles 96 and 89 us).  At least 512 for many units, which need few pieces.
-constexpr int kGroupsMost = 1024;
 int groups_of(int64_t units) {
   if (units <= 64) return 512 - (int)units;
   return units < 512 ? kGroupsMost - (int)units : 512;
