@@ -164,6 +164,16 @@ def test_attend_refuses_bad_calls(lib):
         f = dict(good, **over)
         assert lib.moe_quant_attend(c, f["hq"], f["scale"], f["window"], f["q"], f["table"], f["apart"], f["pages"],
                                     f["lengths"], f["b"], f["out"], f["lse"], f["ws"], f["n"], None) == expect, over
+    # the most requests, and too many of the most heads
+    wide = ctypes.byref(_cache(heads=1024))
+    assert lib.moe_quant_attend_workspace_size(wide, 1024, 1 << 13, ctypes.byref(b)) == OK
+    assert lib.moe_quant_attend_workspace_size(wide, 1024, (1 << 13) + 1, ctypes.byref(b)) == SHAPE
+    assert lib.moe_quant_attend(wide, 1024, 1.0, 0, P, P, 7, 7, P, 1 << 14, P, None, P, 1 << 40, None) == SHAPE
+    # a request of 2^30 tokens, and one page more; a scale that only its product with the keys' makes infinite
+    for pages, ws, expect in ((1 << 26, 0, WORKSPACE), ((1 << 26) + 1, 1 << 40, SHAPE)):
+        assert lib.moe_quant_attend(c, 8, 1.0, 0, P, P, 1 << 27, pages, P, 5, P, None, P, ws, None) == expect
+    assert lib.moe_quant_attend(ctypes.byref(_cache(dtype=1, ks=1e10)), 8, 1e30, 0, P, P, 7, 7, P, 5, P, None, P, 1 << 40,
+                                None) == SHAPE
     assert lib.moe_quant_attend(c, 8, 1.0, 0, None, None, 0, 0, None, 0, None, None, None, 0, None) == OK
 
 

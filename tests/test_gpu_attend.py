@@ -111,10 +111,12 @@ def test_windows(window):
         Case(LENGTHS, page=page, seed=window % 97).check(window=window)
 
 
-@pytest.mark.parametrize("batch", [1, 2, 5, 64, 257, 700])
+@pytest.mark.parametrize("batch", [1, 2, 5, 64, 257, 700, 1024, 1100])
 def test_batches(batch):
     rng = np.random.default_rng(batch)
-    Case([int(n) for n in rng.integers(0, 200 if batch > 100 else 900, batch)], 8, 2, 64, seed=batch).check()
+    lengths = [int(n) for n in rng.integers(0, 200 if batch > 100 else 900, batch)]
+    lengths[batch // 2] = 3000
+    Case(lengths, 8, 2, 64, seed=batch).check()
 
 
 @pytest.mark.parametrize("lengths", [[5000], [40000], [3, 20000, 0, 1], [33000, 31, 32768], [1] * 30 + [9000]])

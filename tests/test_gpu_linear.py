@@ -137,6 +137,23 @@ def test_long_axes(t, n, k):
     check(t, n, k, dtype=F32, seed=n)
 
 
+def test_more_rows_than_a_launch_has_lanes():
+    """2^20 + 5 rows of 64 blocks: more groups of 16 lanes than one pass of the
+    quantization holds."""
+    t, k = (1 << 20) + 5, 8192
+    w, s = make(16, k, 2)
+    x = torch.empty(t, k, dtype=BF, device="cuda")
+    x[:] = rows(1, k, 3)
+    at = [0, 1, 65535, 1 << 19, (1 << 20) - 1, 1 << 20, t - 2, t - 1]
+    some = rows(len(at), k, 4)
+    x[at] = some
+    got = Linear(w, s).forward(x)
+    torch.cuda.synchronize()
+    y, *parts = olin.forward(f64(some), w.cpu().numpy(), s.cpu().numpy())
+    assert np.all(np.abs(f64(got[at]) - y) <= limit(y, *parts, k, BF))
+    assert torch.equal(got[2], got[t - 3]) and torch.equal(got[2], got[1 << 18])
+
+
 def test_rows_of_every_size():
     """Zero rows, rows below the smallest normal number, rows near the largest."""
     for t in (9, 300):

@@ -51,6 +51,10 @@ constexpr int kWaves = 4;
 constexpr int kPlanBatch = 1024;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
+// Heads of a unit at most, and floats of a part of one: R maxima, R sums, O [R, D].
+__host__ __device__ __forceinline__ int rows_of(const AttendArgs &a) { return a.Hq / a.Hk < 16 ? a.Hq / a.Hk : 16; }
+__host__ __device__ __forceinline__ int64_t part_size(const AttendArgs &a) { return rows_of(a) * (int64_t)(a.D + 2); }
+
 // One wave's running state: maximum (in base-2 exponents) and sum for head r
 // (the sum over this lane's tokens), O^T of head r: register i of o[j] is
 // d = (DT / 16) (4 g + i) + j.
@@ -290,10 +294,11 @@ struct Attend {
         y += f * sh.o[w][n][d + 1];
       }
       if (part) {
-        *(float2 *)(part + 32 + n * D + d) = float2{x, y};
+        const int R = rows_of(a);
+        *(float2 *)(part + 2 * R + n * D + d) = float2{x, y};
         if (d == 0) {
           part[n] = m;
-          part[16 + n] = l;
+          part[R + n] = l;
         }
       } else {
         write_out(a, head + n, d, m, l, x, y);
@@ -361,7 +366,7 @@ __device__ __forceinline__ int wave_sum(int v) {
 struct Plan {
   int groups, share_min;   // share: at least share_min tiles
   int *first;              // [B + 1]: number of a request's first piece; of all pieces
-  float *parts;            // per piece, if its unit has others: 16 maxima, 16 sums, O [16, D]
+  float *parts;            // per piece, if its unit has others: R maxima, R sums, O [R, D]
 };
 
 template <int DT, bool FP8>
@@ -402,7 +407,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_pieces_kernel(AttendArg
   const int kt = rel / k, i = rel - kt * k;
   const Span s = span_of(a, a.lengths[b]);
   const Heads h = heads_of(a, b, kt);
-  float *part = plan.parts + blockIdx.x * (32 + 16 * (int64_t)a.D);
+  float *part = plan.parts + blockIdx.x * part_size(a);
   A::unit(a, sh, b, h.kh, h.head, h.nh, s.start, s.end, (int)((int64_t)s.tiles * i / k), (int)((int64_t)s.tiles * (i + 1) / k),
           k == 1 ? nullptr : part);
 }
@@ -421,10 +426,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pla
   const Heads h = heads_of(a, b, kt);
   if (k <= 1 || r >= h.nh) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = a.D;
-  const int64_t size = 32 + 16 * (int64_t)D;
+  const int64_t size = part_size(a);
+  const int R = rows_of(a);
   const float *part = plan.parts + (f0 + kt * k) * size;
   float2 ahead[kAhead];
-  auto values = [&](int w, int d) { return *(const float2 *)(part + w * size + 32 + r * D + d); };
+  auto values = [&](int w, int d) { return *(const float2 *)(part + w * size + 2 * R + r * D + d); };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
     ahead[i] = float2{0.f, 0.f};
@@ -437,7 +443,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pla
   const float mm = m == -INFINITY ? 0.f : m;
   for (int w = lane; w < k; w += 64) {
     const float f = __builtin_amdgcn_exp2f(part[w * size + r] - mm);
-    l += part[w * size + 16 + r] * f;
+    l += part[w * size + R + r] * f;
     if (wave == 0) weight[w] = f;
   }
 #pragma unroll
@@ -493,8 +499,11 @@ int share_min_of(int64_t units) { return units / 8 < 4 ? 4 : units / 8 > 128 ? 1
 static size_t first_bytes(int64_t B) { return ((size_t)(B + 1) * 4 + 255) / 256 * 256; }
 
 size_t attend_workspace(int64_t B, int Hq, int Hk, int D) {
+  if (B > kPlanBatch) return 256;   // no pieces
+  AttendArgs a{};
+  a.Hq = Hq; a.Hk = Hk; a.D = D;
   const int64_t units = B * Hk * ((Hq / Hk + 15) / 16);
-  return first_bytes(B) + (size_t)(groups_of(units) + units) * (32 + 16 * (size_t)D) * 4;
+  return first_bytes(B) + ((size_t)(groups_of(units) + units) * part_size(a) * 4 + 255) / 256 * 256;
 }
 
 template <int DT, bool FP8>
@@ -502,7 +511,8 @@ static hipError_t run_attend(const AttendArgs &a, hipStream_t s) {
   const int G = a.Hq / a.Hk;
   const unsigned units = (unsigned)a.B * a.Hk * ((G + 15) / 16);
   const int share_min = share_min_of(units), groups = groups_of(units);
-  const int most = a.window && a.window < a.max_tokens ? (a.window + 2 * (kTile - 1)) / kTile : (a.max_tokens + kTile - 1) / kTile;
+  // tiles of a unit at most; a window may end inside of one at either end
+  const int tokens = a.window && a.window < a.max_tokens ? a.window + kTile - 1 : a.max_tokens, most = (tokens + kTile - 1) / kTile;
   if (most <= share_min || a.B > kPlanBatch) {
     attend_units_kernel<DT, FP8><<<dim3(units), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();

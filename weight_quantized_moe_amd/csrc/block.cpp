@@ -104,6 +104,14 @@ mq_status check_heads(const mq_kv_cache *c, int32_t q_heads, const char *who) {
   return MQ_OK;
 }
 
+mq_status check_units(const mq_kv_cache *c, int32_t q_heads, int64_t batch, const char *who) {
+  const int64_t units = batch * c->kv_heads * ((q_heads / c->kv_heads + 15) / 16);
+  if (units > mq::kMaxUnits)
+    return fail(MQ_E_SHAPE, "%s: batch %lld times %lld groups of up to 16 query heads exceed %lld", who, (long long)batch,
+                (long long)(units / batch), (long long)mq::kMaxUnits);
+  return MQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -198,6 +206,7 @@ mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads,
   mq_status st = check_cache(c, "attend_workspace_size");
   if (st == MQ_OK) st = check_heads(c, q_heads, "attend_workspace_size");
   if (st == MQ_OK) st = check_batch(batch, "attend_workspace_size");
+  if (st == MQ_OK) st = check_units(c, q_heads, batch, "attend_workspace_size");
   if (st != MQ_OK) return st;
   if (!bytes) return fail(MQ_E_NULL, "attend_workspace_size: NULL argument");
   *bytes = mq::attend_workspace(batch, q_heads, c->kv_heads, c->head_dim);
@@ -212,11 +221,13 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
   mq_status st = check_cache(c, "attend");
   if (st == MQ_OK) st = check_heads(c, q_heads, "attend");
   if (st == MQ_OK) st = check_batch(batch, "attend");
+  if (st == MQ_OK) st = check_units(c, q_heads, batch, "attend");
   if (st != MQ_OK) return st;
-  if (!std::isfinite(scale)) return fail(MQ_E_SHAPE, "attend: scale %g must be finite", (double)scale);
+  if (!std::isfinite(scale) || !std::isfinite(scale * c->k_scale))
+    return fail(MQ_E_SHAPE, "attend: scale %g (times k_scale %g) must be finite", (double)scale, (double)c->k_scale);
   if (window < 0) return fail(MQ_E_SHAPE, "attend: window %d must not be negative", window);
-  if (max_pages < 0 || max_pages > INT32_MAX / c->page_size || table_stride < max_pages)
-    return fail(MQ_E_SHAPE, "attend: max_pages %d times page_size must be below 2^31, table_stride %lld at least "
+  if (max_pages < 0 || max_pages > mq::kMaxRequest / c->page_size || table_stride < max_pages)
+    return fail(MQ_E_SHAPE, "attend: max_pages %d times page_size must be at most 2^30, table_stride %lld at least "
                 "max_pages", max_pages, (long long)table_stride);
   if (batch == 0) {
     mq::clear_error();

@@ -211,7 +211,9 @@ struct KvAppendArgs {
   float eps, k_scale, v_scale;
 };
 constexpr int kMaxHeads = 1024;
-constexpr int64_t kMaxBatch = 1 << 16;  // requests of one attention
+constexpr int64_t kMaxBatch = 1 << 16;     // requests of one attention
+constexpr int64_t kMaxUnits = 1 << 23;     // requests times groups of 16 query heads that share a key head
+constexpr int kMaxRequest = 1 << 30;       // tokens that a request's pages hold at most
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 
 struct AttendArgs {

@@ -192,22 +192,10 @@ void run_append(const KvAppendArgs &a, hipStream_t s) {
   // leave kWaves of them
   const int want = (int)((kWaves + a.T - 1) / a.T), most_parts = want < groups ? want : groups;
   const int turns = (groups + most_parts - 1) / most_parts, parts = (groups + turns - 1) / turns;
-  const int64_t most = ((int64_t)1 << 28) / parts;   // wave numbers stay in 32 bits
-  for (int64_t t = 0; t < a.T; t += most) {
-    KvAppendArgs p = a;
-    p.T = a.T - t < most ? a.T - t : most;
-    if (p.q) {
-      p.q += t * a.q_stride;
-      p.q_out += t * a.Hq * a.D;
-    }
-    p.k += t * a.k_stride;
-    p.v += t * a.v_stride;
-    p.slots += t;
-    if (p.positions) p.positions += t;
-    const dim3 grid((unsigned)((p.T * parts + 3) / 4)), block(256);
-    if (a.fp8) kv_append_kernel<LP, true><<<grid, block, 0, s>>>(p, parts, turns);
-    else kv_append_kernel<LP, false><<<grid, block, 0, s>>>(p, parts, turns);
-  }
+  // T parts is below T + kWaves, so wave numbers and lanes stay in 32 bits
+  const dim3 grid((unsigned)((a.T * parts + 3) / 4)), block(256);
+  if (a.fp8) kv_append_kernel<LP, true><<<grid, block, 0, s>>>(a, parts, turns);
+  else kv_append_kernel<LP, false><<<grid, block, 0, s>>>(a, parts, turns);
 }
 
 }  // namespace

@@ -105,16 +105,20 @@ __device__ __forceinline__ u2 quantize8(u4 v, float *scale) {
   return c;
 }
 
+// Workgroups of a launch, of at most 512 lanes: a grid has fewer than 2^32 lanes.
+constexpr int64_t kMostGroups = (1 << 23) - 8;
+constexpr int64_t kQuantGroups = 1 << 22;   // workgroups at most: 2^30 lanes
+
 __global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t grp = id >> 4;
-  if (grp >= a.T * a.G) return;  // 16 lanes at a time, so the shuffles stay among live lanes
-  const int64_t t = grp / a.G;
-  const int g = (int)(grp - t * a.G), at = g * 128 + 8 * (int)(id & 15);
-  float s;
-  const u2 c = quantize8(at < a.K ? *(const u4 *)(a.x + t * a.K + at) : u4{0u, 0u, 0u, 0u}, &s);
-  *(u2 *)(a.codes + t * (a.G * (int64_t)128) + at) = c;
-  if ((id & 15) == 0) a.sa[g * a.T + t] = s;
+  // 16 lanes at a time, so the shuffles stay among live lanes
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < a.T * a.G * 16; id += (int64_t)gridDim.x * 256) {
+    const int64_t grp = id >> 4, t = grp / a.G;
+    const int g = (int)(grp - t * a.G), at = g * 128 + 8 * (int)(id & 15);
+    float s;
+    const u2 c = quantize8(at < a.K ? *(const u4 *)(a.x + t * a.K + at) : u4{0u, 0u, 0u, 0u}, &s);
+    *(u2 *)(a.codes + t * (a.G * (int64_t)128) + at) = c;
+    if ((id & 15) == 0) a.sa[g * a.T + t] = s;
+  }
 }
 
 // out[t, n .. n + W) = round(y + residual); fast: all W there and rows 16-byte aligned
@@ -478,7 +482,7 @@ template <bool kExact, int WM, int WN, int TM, int STAGES>
 hipError_t run_tiles(const LinearArgs &a, hipStream_t s) {
   using L = Tile<WM, WN, TM, STAGES>;
   const int64_t all = ((a.T + L::BM - 1) / L::BM) * ((a.N + L::BN - 1) / L::BN);
-  if (all > 0x7FFFFFF0) return hipErrorInvalidConfiguration;
+  if (all > kMostGroups) return hipErrorInvalidConfiguration;
   raise_lds_limit((const void *)linear_tiles_kernel<kExact, WM, WN, TM, STAGES>);
   linear_tiles_kernel<kExact, WM, WN, TM, STAGES>
       <<<dim3((unsigned)((all + 7) / 8 * 8)), dim3(64 * L::kWaves), L::lds(a.G), s>>>(a);
@@ -488,7 +492,7 @@ hipError_t run_tiles(const LinearArgs &a, hipStream_t s) {
 template <bool kExact, int NT, int MT, int U, bool kFused>
 hipError_t run_stream(const LinearArgs &a, hipStream_t s) {
   const int64_t wgs = (int64_t)((a.N + 16 * NT - 1) / (16 * NT)) * ((a.T + 16 * MT - 1) / (16 * MT));
-  if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if (wgs > kMostGroups) return hipErrorInvalidConfiguration;
   const size_t lds = kFused ? a.T * (a.G * (size_t)128 + 16 + a.G * 4) : 0;
   linear_stream_kernel<kExact, NT, MT, U, kFused><<<dim3((unsigned)wgs), dim3(64 * kStreamWaves), lds, s>>>(a);
   return hipGetLastError();
@@ -498,8 +502,7 @@ template <bool kExact>
 hipError_t run_linear(const LinearArgs &a, hipStream_t s) {
   if (a.T <= 16 && a.T * a.G <= kFusedBlocks) return run_stream<kExact, 1, 1, 1, true>(a, s);
   const int64_t quant = (a.T * a.G * 16 + 255) / 256;
-  if (quant > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  linear_quant_kernel<<<dim3((unsigned)quant), dim3(256), 0, s>>>(a);
+  linear_quant_kernel<<<dim3((unsigned)(quant < kQuantGroups ? quant : kQuantGroups)), dim3(256), 0, s>>>(a);
   auto cover = [&](int bm, int bn) { return ((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   if (a.T <= 64 || cover(64, 32) <= kStreamMost) {
     if (a.T > 32 && cover(64, 32) >= kStreamLeast) return run_stream<kExact, 2, 4, 2, false>(a, s);
