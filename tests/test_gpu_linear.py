@@ -90,8 +90,9 @@ def test_sizes(t, n, k, dtype):
 
 
 @pytest.mark.parametrize("t,n,k", [(10, 4999, 2064), (16, 4900, 1040), (20, 4999, 400), (33, 5000, 272), (64, 4801, 2064),
-                                   (130, 1700, 400), (200, 2400, 144),      # streamed, 32 weight rows a workgroup
-                                   (70, 7000, 144), (333, 2000, 400),       # tiles of 64 x 64
+                                   (130, 1300, 400), (200, 960, 144),       # streamed, 32 weight rows a workgroup
+                                   (130, 4000, 144), (333, 2000, 400), (300, 2300, 1040),   # 64 x 64, 4 blocks of K at a time
+                                   (70, 9000, 144), (600, 2000, 400),       # tiles of 64 x 64
                                    (2049, 2100, 272),                       # tiles of 64 x 128
                                    (2050, 2570, 144)])                      # tiles of 128 x 128
 @pytest.mark.parametrize("dtype", [BF, F32])

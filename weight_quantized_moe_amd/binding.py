@@ -743,14 +743,14 @@ class KVCache:
     def _heads(self, t, name, tokens, heads):
         """Token stride of ``t`` [T, heads, D]: heads side by side, tokens any number of values apart."""
         d = self.head_dim
-        if t.dtype is not self._q.bf16 or t.shape != (tokens, heads, d) or t.get_device() != self._index:
+        step, hs, ds = t.stride()
+        if not (t.dtype is self._q.bf16 and t.shape == (tokens, heads, d) and t.get_device() == self._index and ds == 1
+                and (hs == d or heads == 1)):
             if t.dtype is not self._q.bf16:
                 raise ValueError(f"{name} has dtype {t.dtype}, expected {self._q.bf16}")
             if t.shape != (tokens, heads, d):
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
             _on_gpu(self.device, **{name: t})
-        step, hs, ds = t.stride()
-        if (ds != 1 and d > 1) or (hs != d and heads > 1):
             raise ValueError(f"the heads of {name} must lie one behind the other")
         return step if tokens > 1 else heads * d
 
@@ -761,8 +761,8 @@ class KVCache:
         [T] (not used without a rotation).  The heads of a token lie side by side, tokens
         any multiple of 8 values apart, so all three may be views of one fused
         projection.  Returns ``q_out`` [T, q_heads, D] (None without queries)."""
-        if k.dim() != 3:
-            raise ValueError("k must be [T, kv_heads, D]")
+        if k.dim() != 3 or v.dim() != 3:
+            raise ValueError("k and v must be [T, kv_heads, D]")
         w, index, t = self._q, self._index, k.shape[0]
         if index != w.device_now():
             with w.on(index):

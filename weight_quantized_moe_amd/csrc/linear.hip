@@ -171,11 +171,6 @@ __device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, con
 // while its first weights are on their way; else the codes are read from the
 // workspace.
 constexpr int kStreamWaves = 8;
-// Blocks of 128 that a workgroup quantizes itself at most.
-constexpr int kFusedBlocks = 128;
-// Fewest workgroups for a larger part of the result to each, and most of them for
-// which the axis K over the waves of a workgroup still beats tiles in LDS.
-constexpr int64_t kStreamLeast = 150, kStreamMost = 256;
 
 template <bool kExact, int NT, int MT, int U, bool kFused>
 __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(LinearArgs a) {
@@ -284,7 +279,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 }
 
 // ---- many tokens: tiles of BM tokens x BN weight rows, WM x WN waves, each with
-// TM x 4 results of 16 x 16.
+// TM x 4 results of 16 x 16; KS times as many waves take KS blocks of K at a time,
+// and their sums are added at the end.
 //
 // A k step is one block of 128: BM rows of activation codes, BN of weight codes (128
 // bytes each) and BM activation scales, copied from global memory straight into
@@ -312,26 +308,27 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-template <int WM, int WN, int TM, int STAGES>
+template <int WM, int WN, int TM, int STAGES, int KS>
 struct Tile {
   static constexpr int kWaves = WM * WN, BM = WM * TM * 16, BN = WN * 64;
   static constexpr int kStages = STAGES;
   static constexpr int kTokenCopies = BM / 8 / kWaves, kWeightCopies = BN / 8 / kWaves;  // per wave and step, 1 KB each
   static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "waves copy whole groups of 8 rows");
   static constexpr int kScaleRows = BM < 64 ? 64 : BM;             // copied 64 at a time
-  static constexpr int kStageBytes = (BM + BN) * 128 + kScaleRows * 4;
+  static constexpr int kBlockBytes = (BM + BN) * 128 + kScaleRows * 4, kStageBytes = KS * kBlockBytes;
   static constexpr int kBlocks = (BN + 127) / 128;                 // weight blocks that a tile may touch
   static constexpr int lds(int G) { return kStages * kStageBytes + kBlocks * G * 4; }
 };
 
-template <bool kExact, int WM, int WN, int TM, int STAGES>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
+template <bool kExact, int WM, int WN, int TM, int STAGES, int KS>
+__global__ __launch_bounds__(64 * WM * WN * KS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void linear_tiles_kernel(LinearArgs a) {
-  using L = Tile<WM, WN, TM, STAGES>;
+  using L = Tile<WM, WN, TM, STAGES, KS>;
   constexpr int BM = L::BM, BN = L::BN, kStages = L::kStages, CX = L::kTokenCopies, CW = L::kWeightCopies;
   extern __shared__ __align__(16) unsigned char smem[];
   float *sws = (float *)(smem + kStages * L::kStageBytes);
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int ks = all_waves / L::kWaves, wave = all_waves - ks * L::kWaves;
   const int G = a.G, K = a.K;
   const int64_t Kp = G * (int64_t)128;
   // ---- tile of this workgroup.  The 8 XCDs take contiguous ranges; inside a range
@@ -347,7 +344,7 @@ void linear_tiles_kernel(LinearArgs a) {
   const int n0 = in / high * BN;
   // ---- weight scales of the tile's blocks (0 past the end)
   const int nb = (a.N + 127) / 128;
-  for (int i = tid; i < L::kBlocks * G; i += 64 * L::kWaves) {
+  for (int i = tid; i < L::kBlocks * G; i += 64 * L::kWaves * KS) {
     const int b = i / G, g = i - b * G, at = n0 / 128 + b;
     sws[i] = at < nb ? a.scale[(int64_t)at * G + g] : 0.f;
   }
@@ -371,8 +368,11 @@ void linear_tiles_kernel(LinearArgs a) {
   // activation scales: wave w copies those of tokens 64 (w % (kScaleRows / 64)) + [0, 64)
   const int sg = wave % (L::kScaleRows / 64);
   const float *sbase = a.sa + min(t0 + 64 * sg + lane, a.T - 1);
-  auto issue = [&](int g) {
-    unsigned char *st = smem + (g % kStages) * L::kStageBytes;
+  // steps of the axis: block KS g + ks, the last one again behind the end (times 0)
+  const int steps = (G + KS - 1) / KS;
+  auto issue = [&](int step) {
+    unsigned char *st = smem + (step % kStages) * L::kStageBytes + ks * L::kBlockBytes;
+    const int g = KS == 1 ? step : min(KS * step + ks, G - 1);
     const uint8_t *xg = xbase + g * 128, *wg = wbase + g * 128;
 #pragma unroll
     for (int p = 0; p < CX; ++p) dma16(xg + xoff[p], st + 1024 * (CX * wave + p));
@@ -403,10 +403,11 @@ void linear_tiles_kernel(LinearArgs a) {
   // One k step: the next token rows' operand and the sums of the rows before are in
   // work while the matrix units multiply (the barriers keep the compiler from
   // putting each read right in front of its use).
-  auto compute = [&](int g) {
-    const unsigned char *st = smem + (g % kStages) * L::kStageBytes, *ws = st + BM * 128;
+  auto compute = [&](int step) {
+    const unsigned char *st = smem + (step % kStages) * L::kStageBytes + ks * L::kBlockBytes, *ws = st + BM * 128;
     const float *ss = (const float *)(st + (BM + BN) * 128);
-    const float f = sws[blk * G + g];
+    const int g = KS * step + ks;
+    const float f = KS == 1 || g < G ? sws[blk * G + g] : 0.f;
     auto token = [&](int m, Frag<kExact> &b) {
       const int t = tok + 16 * m, z = (t >> 1) & 7;
       b.set(*(const u4 *)(st + t * 128 + 16 * (q ^ z)), *(const u4 *)(st + t * 128 + 16 * ((q + 4) ^ z)));
@@ -447,19 +448,39 @@ void linear_tiles_kernel(LinearArgs a) {
     }
   };
   __syncthreads();   // the weight scales; nothing else is in flight yet
-  for (int g = 0; g < kStages - 1 && g < G; ++g) issue(g);
-  for (int g = 0; g < G; ++g) {
+  for (int g = 0; g < kStages - 1 && g < steps; ++g) issue(g);
+  for (int g = 0; g < steps; ++g) {
     // step g's copies have landed (later ones stay in flight), for every wave; and
     // every wave is done with step g - 1, whose stage the next copies fill
-    if (kStages > 2 && g + kStages - 2 < G)
+    if (kStages > 2 && g + kStages - 2 < steps)
       wait_vm<(kStages - 2) * (CX + CW + 1)>();
     else
       wait_vm<0>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (g + kStages - 1 < G) issue(g + kStages - 1);
+    if (g + kStages - 1 < steps) issue(g + kStages - 1);
     compute(g);
+  }
+  // ---- the other blocks' sums, through LDS
+  if constexpr (KS > 1) {
+    static_assert((KS - 1) * BM * BN * 4 <= kStages * L::kStageBytes, "sums fit the stages");
+    f4 *sums = (f4 *)smem;
+    __syncthreads();   // every wave is done with the stages
+    if (ks > 0) {
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[(((ks - 1) * L::kWaves + wave) * TM * 4 + 4 * m + j) * 64 + lane] = acc[m][j];
+    }
+    __syncthreads();
+    if (ks > 0) return;
+#pragma unroll
+    for (int o = 0; o < KS - 1; ++o)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] += sums[((o * L::kWaves + wave) * TM * 4 + 4 * m + j) * 64 + lane];
   }
   // ---- results: token tok + 16 m, weight rows 64 wn + 16 q + [0, 16)
   const int n = n0 + wn * 64 + 16 * q;
@@ -478,14 +499,14 @@ void linear_tiles_kernel(LinearArgs a) {
   }
 }
 
-template <bool kExact, int WM, int WN, int TM, int STAGES>
+template <bool kExact, int WM, int WN, int TM, int STAGES, int KS = 1>
 hipError_t run_tiles(const LinearArgs &a, hipStream_t s) {
-  using L = Tile<WM, WN, TM, STAGES>;
+  using L = Tile<WM, WN, TM, STAGES, KS>;
   const int64_t all = ((a.T + L::BM - 1) / L::BM) * ((a.N + L::BN - 1) / L::BN);
   if (all > kMostGroups) return hipErrorInvalidConfiguration;
-  raise_lds_limit((const void *)linear_tiles_kernel<kExact, WM, WN, TM, STAGES>);
-  linear_tiles_kernel<kExact, WM, WN, TM, STAGES>
-      <<<dim3((unsigned)((all + 7) / 8 * 8)), dim3(64 * L::kWaves), L::lds(a.G), s>>>(a);
+  raise_lds_limit((const void *)linear_tiles_kernel<kExact, WM, WN, TM, STAGES, KS>);
+  linear_tiles_kernel<kExact, WM, WN, TM, STAGES, KS>
+      <<<dim3((unsigned)((all + 7) / 8 * 8)), dim3(64 * L::kWaves * KS), L::lds(a.G), s>>>(a);
   return hipGetLastError();
 }
 
@@ -498,24 +519,43 @@ hipError_t run_stream(const LinearArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which way, by how many workgroups of each form there would be (us of a whole call
+// from Python, K = 2048 unless said; one launch from the host takes 2.4, quantizing
+// beforehand 2 to 3 more).
 template <bool kExact>
 hipError_t run_linear(const LinearArgs &a, hipStream_t s) {
-  if (a.T <= 16 && a.T * a.G <= kFusedBlocks) return run_stream<kExact, 1, 1, 1, true>(a, s);
+  // few tokens: every workgroup quantizes what it needs (1 x 5120: 4.9, quantized
+  // beforehand 7.2; 8 x 2048: 5.9 and 6.9), up to 128 blocks (16 x 5120, 256 of them:
+  // 10.6 and 8.1)
+  if (a.T <= 16 && a.T * a.G <= 128) return run_stream<kExact, 1, 1, 1, true>(a, s);
   const int64_t quant = (a.T * a.G * 16 + 255) / 256;
   linear_quant_kernel<<<dim3((unsigned)(quant < kQuantGroups ? quant : kQuantGroups)), dim3(256), 0, s>>>(a);
   auto cover = [&](int bm, int bn) { return ((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if (a.T <= 64 || cover(64, 32) <= kStreamMost) {
-    if (a.T > 32 && cover(64, 32) >= kStreamLeast) return run_stream<kExact, 2, 4, 2, false>(a, s);
-    if (a.T > 16 && cover(32, 32) >= kStreamLeast) return run_stream<kExact, 2, 2, 2, false>(a, s);
-    if (cover(16, 32) >= kStreamLeast) return run_stream<kExact, 2, 1, 2, false>(a, s);
+  // streamed: the largest part of the result that still leaves 150 workgroups (64 x
+  // 5120: 11.3 with parts of 64 x 32, 13.1 of 16 x 32, 14.3 of 16 x 16; 32 x 2048, K 4096:
+  // 8.6 of 16 x 16, 10.2 of 16 x 32), for up to 64 tokens and up to 128 parts of 64 x 32
+  // (128 x 2048: 9.0, tiles 10.5; 256 x 2048: 11.7, tiles 10.9)
+  if (a.T <= 64 || cover(64, 32) <= 128) {
+    if (a.T > 32 && cover(64, 32) >= 150) return run_stream<kExact, 2, 4, 2, false>(a, s);
+    if (a.T > 16 && cover(32, 32) >= 150) return run_stream<kExact, 2, 2, 2, false>(a, s);
+    if (cover(16, 32) >= 150) return run_stream<kExact, 2, 1, 2, false>(a, s);
     return run_stream<kExact, 1, 1, 2, false>(a, s);
   }
+  // 256 x 256, a workgroup a CU: four rounds of them at least (16384 x 5120: 205, in
+  // tiles of 128 x 128 221; 4096 x 5120, 1.25 rounds: 78 and 62).  Its registers do not
+  // hold the FP16 operands.
   if constexpr (!kExact) {
     if (cover(256, 256) >= 1024) return run_tiles<false, 2, 4, 8, 2>(a, s);
   }
+  // 128 x 128 and 64 x 128, two a CU (1024 x 5120, 320 and 640 of them: 26.5 and 28.4;
+  // 2048 x 2048, 256 and 512: 23.8 and 21.6)
   if (cover(128, 128) >= 320) return run_tiles<kExact, 2, 2, 4, 2>(a, s);
   if (cover(64, 128) >= 512) return run_tiles<kExact, 2, 2, 2, 3>(a, s);
-  return run_tiles<kExact, 4, 1, 1, 4>(a, s);
+  // 64 x 64: two a CU where there are more than CUs (256 x 5120, 320 of them: 13.7), else
+  // one, whose 16 waves take four blocks of K at a time (16.8; 128 x 5120, 160: 10.6,
+  // two a CU 11.9; 512 x 2048, K 4096: 16.6 and 20.4)
+  if (cover(64, 64) > 256) return run_tiles<kExact, 4, 1, 1, 4>(a, s);
+  return run_tiles<kExact, 4, 1, 1, 2, 4>(a, s);
 }
 
 }  // namespace
