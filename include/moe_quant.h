@@ -512,8 +512,9 @@ mq_status moe_quant_linear_workspace_size(const mq_linear *l, int64_t num_tokens
 /*
  * Enqueue the product of num_tokens rows on `stream`.
  *   x_bf16        [T, K] BF16 bits, 16-byte aligned
- *   residual_bf16 NULL, or [T, N] BF16 bits, 2-byte aligned; may alias out
- *   out           [T, N] of out_dtype, aligned to its element
+ *   residual_bf16 NULL, or [T, N] BF16 bits, 2-byte aligned
+ *   out           [T, N] of out_dtype, aligned to its element; a BF16 one may be
+ *                 residual_bf16 itself; otherwise it overlaps neither input
  *   workspace     >= moe_quant_linear_workspace_size bytes, 256-byte aligned; its
  *                 contents on entry do not matter
  * num_tokens == 0 returns MQ_OK without enqueuing anything.
@@ -577,7 +578,7 @@ typedef struct {
  *               is negative or behind the cache, or whose position is not a row of
  *               cos_sin, is padding: nothing of it is written
  *   q_out       [T, q_heads, D] BF16 bits, 16-byte aligned; may be q itself where
- *               q_stride is q_heads * D
+ *               q_stride is q_heads * D, and does not overlap q, k and v otherwise
  * MQ_KV_FP8 keeps RNE-to-E4M3(value / scale), saturated to +-448.  The slots of
  * one call are distinct: of a slot given twice it is unspecified which token's
  * values stay, per 8 values.
@@ -611,7 +612,8 @@ mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads,
  *               is not read into the result
  *   lengths     int32 [B]; below 1 the request is empty: out 0, lse -inf.  More
  *               than max_pages pages hold counts as what they hold
- *   out_bf16    [B, q_heads, D] BF16 bits, 16-byte aligned; may alias q_bf16
+ *   out_bf16    [B, q_heads, D] BF16 bits, 16-byte aligned; may be q_bf16 itself, and
+ *               does not overlap it otherwise
  *   lse         NULL, or float [B, q_heads], 4-byte aligned
  *   workspace   >= moe_quant_attend_workspace_size bytes, 256-byte aligned; its
  *               contents on entry do not matter

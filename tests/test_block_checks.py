@@ -77,14 +77,19 @@ def test_linear_refuses_bad_calls(lib):
     r = ctypes.byref(d)
     assert lib.moe_quant_linear_workspace_size(r, 3, ctypes.byref(b)) == OK and b.value > 0
     assert lib.moe_quant_linear_workspace_size(r, 3, None) == NULL
+    Q = 2 * P                                        # apart from x
     assert lib.moe_quant_linear_workspace_size(r, -1, ctypes.byref(b)) == SHAPE
     assert lib.moe_quant_linear_workspace_size(r, (1 << 22) + 1, ctypes.byref(b)) == SHAPE
-    for args, expect in (((P, None, -1, P, P, b.value), SHAPE), ((P, None, (1 << 22) + 1, P, P, b.value), SHAPE),
-                         ((None, None, 3, P, P, b.value), NULL), ((P, None, 3, None, P, b.value), NULL),
-                         ((P + 8, None, 3, P, P, b.value), ALIGN), ((P, P + 1, 3, P, P, b.value), ALIGN),
-                         ((P, None, 3, P + 1, P, b.value), ALIGN), ((P, None, 3, P, None, b.value), WORKSPACE),
-                         ((P, None, 3, P, P + 16, b.value), ALIGN), ((P, None, 3, P, P, b.value - 1), WORKSPACE)):
+    for args, expect in (((P, None, -1, Q, P, b.value), SHAPE), ((P, None, (1 << 22) + 1, Q, P, b.value), SHAPE),
+                         ((None, None, 3, Q, P, b.value), NULL), ((P, None, 3, None, P, b.value), NULL),
+                         ((P + 8, None, 3, Q, P, b.value), ALIGN), ((P, P + 1, 3, Q, P, b.value), ALIGN),
+                         ((P, None, 3, Q + 1, P, b.value), ALIGN), ((P, None, 3, Q, None, b.value), WORKSPACE),
+                         ((P, None, 3, Q, P + 16, b.value), ALIGN), ((P, None, 3, Q, P, b.value - 1), WORKSPACE)):
         assert lib.moe_quant_linear(r, *args, None) == expect, args
+    # n 128, k 256, 3 rows: x takes 0x600 bytes, a BF16 out and the residual 0x300
+    for x, res, out in ((P, None, P), (P, None, P + 0x5FE), (P + 0x2F0, None, P), (P, 9 * P, 9 * P + 2), (P, 9 * P + 0x2FE, 9 * P)):
+        assert lib.moe_quant_linear(r, x, res, 3, out, 99 * P, b.value, None) == SHAPE, (x, res, out)
+    assert lib.moe_quant_linear(ctypes.byref(_linear(out=0)), P, 9 * P, 3, 9 * P, 99 * P, b.value, None) == SHAPE
     assert lib.moe_quant_linear(None, P, None, 3, P, P, b.value, None) == NULL
     f = _linear(out=0)
     assert lib.moe_quant_linear(ctypes.byref(f), P, None, 3, P + 2, P, b.value, None) == ALIGN
@@ -133,6 +138,7 @@ def test_rotary_refuses_bad_fields(lib, over, expect):
 
 def test_append_refuses_bad_calls(lib):
     c, r = ctypes.byref(_cache()), ctypes.byref(_rotary())
+    # q and q_out take 0xC00 bytes, k and v 0x600
     good = dict(hq=8, q=P, qs=512, k=P, ks=256, v=P, vs=256, pos=P, slots=P, t=3, out=2 * P)
     for over, expect in ((dict(t=-1), SHAPE), (dict(t=(1 << 22) + 1), SHAPE), (dict(hq=-1), SHAPE), (dict(hq=1025), SHAPE),
                          (dict(q=None), NULL), (dict(out=None), NULL), (dict(hq=0), NULL), (dict(k=None), NULL),
@@ -140,7 +146,9 @@ def test_append_refuses_bad_calls(lib):
                          (dict(k=P + 4), ALIGN), (dict(v=P + 2), ALIGN), (dict(out=P + 8), ALIGN), (dict(pos=P + 2), ALIGN),
                          (dict(slots=P + 1), ALIGN), (dict(qs=504), SHAPE), (dict(ks=248), SHAPE), (dict(vs=0), SHAPE),
                          (dict(vs=-256), SHAPE), (dict(qs=516), ALIGN), (dict(ks=260), ALIGN), (dict(vs=257), ALIGN),
-                         (dict(qs=1024, out=P), SHAPE)):
+                         (dict(qs=1024, out=P), SHAPE), (dict(out=P), SHAPE), (dict(out=P + 16, k=9 * P, v=9 * P), SHAPE),
+                         (dict(k=2 * P + 0xBF0), SHAPE), (dict(v=2 * P - 0x5F0), SHAPE),
+                         (dict(q=2 * P, out=2 * P, vs=1 << 16), SHAPE)):
         f = dict(good, **over)
         assert lib.moe_quant_kv_append(c, r, f["hq"], f["q"], f["qs"], f["k"], f["ks"], f["v"], f["vs"], f["pos"],
                                        f["slots"], f["t"], f["out"], None) == expect, over
@@ -160,7 +168,8 @@ def test_attend_refuses_bad_calls(lib):
                          (dict(b=(1 << 16) + 1), SHAPE), (dict(q=None), NULL), (dict(table=None), NULL),
                          (dict(lengths=None), NULL), (dict(out=None), NULL), (dict(q=P + 8), ALIGN), (dict(out=P + 8), ALIGN),
                          (dict(table=P + 2), ALIGN), (dict(lengths=P + 1), ALIGN), (dict(lse=P + 2), ALIGN),
-                         (dict(ws=None), WORKSPACE), (dict(ws=P + 128), ALIGN), (dict(n=b.value - 1), WORKSPACE)):
+                         (dict(out=P + 16), SHAPE), (dict(out=P - 16), SHAPE), (dict(ws=None), WORKSPACE),
+                         (dict(ws=P + 128), ALIGN), (dict(n=b.value - 1), WORKSPACE)):
         f = dict(good, **over)
         assert lib.moe_quant_attend(c, f["hq"], f["scale"], f["window"], f["q"], f["table"], f["apart"], f["pages"],
                                     f["lengths"], f["b"], f["out"], f["lse"], f["ws"], f["n"], None) == expect, over

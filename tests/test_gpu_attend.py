@@ -253,6 +253,42 @@ def test_graph_replays_follow_the_lengths():
     c.lengths.copy_(full)
 
 
+def test_two_graphs_of_one_workspace_and_two_host_threads():
+    import threading
+    cases = [Case([9000, 3], 8, 2, 128, seed=16), Case([700, 50, 2000, 0, 40], 8, 2, 128, seed=17)]
+    want = [c.cache.attend(c.q, c.table, c.lengths) for c in cases]
+    ws = cases[1].cache.attend_workspace(5, 8)
+    ws = ws if ws.numel() >= cases[0].cache.attend_workspace_size(2, 8) else cases[0].cache.attend_workspace(2, 8)
+    outs, graphs = [torch.empty_like(o) for o in want], []
+    for c, o in zip(cases, outs):
+        c.cache.attend(c.q, c.table, c.lengths, out=o, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.cache.attend(c.q, c.table, c.lengths, out=o, workspace=ws)
+    for rep in range(3):
+        for o in outs:
+            o.zero_()
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    bad = []
+
+    def work(i):
+        c = cases[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = c.cache.attend(c.q, c.table, c.lengths)
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(got, want[i]):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i % 2,)) for i in range(4)]
+    [x.start() for x in threads], [x.join() for x in threads]
+    assert not bad
+
+
 def test_join_by_lse():
     """Two parts of a request, joined by their lse, are the whole."""
     c = Case([600], 4, 2, 64, page=32, seed=14)

@@ -189,6 +189,30 @@ def test_ties_of_the_codes():
         check(t, 192, 256, F32, x=x.to(BF))
 
 
+def test_codes_are_the_definitions():
+    """The quantized rows as they lie in the workspace (codes [T, 128 G], then the scales
+    [G, T]), for values of every exponent and for blocks whose largest is any BF16
+    mantissa, where many quotients lie midway between two codes."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    t, k = 6000, 400
+    bits = torch.randint(0, 1 << 16, (t, k), generator=gen, device="cuda")
+    bits = torch.where((bits & 0x7F80) == 0x7F80, bits & 0x7F7F, bits)            # finite
+    near = (torch.randint(0, 1 << 7, (t, k), generator=gen, device="cuda")
+            | (torch.randint(118, 128, (t, k), generator=gen, device="cuda") << 7)
+            | (torch.randint(0, 2, (t, k), generator=gen, device="cuda") << 15))
+    bits[t // 3:] = near[t // 3:]
+    x = bits.to(torch.int32).to(torch.int16).view(BF)
+    lin = Linear(*make(64, k))
+    ws = lin.workspace(t)
+    lin.forward(x, workspace=ws)
+    torch.cuda.synchronize()
+    codes, sa = olin.quantize_rows(f64(x))
+    got = ws[:t * 512].view(t, 512).cpu().numpy()
+    assert np.array_equal(got & 127, codes & 127) and np.array_equal((got >> 7)[codes & 127 > 0], (codes >> 7)[codes & 127 > 0])
+    at = -(-t * 512 // 256) * 256
+    assert np.array_equal(ws[at:at + 4 * 4 * t].view(F32).view(4, t).cpu().numpy().T, sa)
+
+
 def test_a_nan_weight_stays_in_its_column():
     for t, k in ((3, 400), (300, 400), (300, 512)):
         w, s = make(300, k)
@@ -259,6 +283,41 @@ def test_streams_and_two_workspaces():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_two_graphs_of_one_workspace_and_two_host_threads():
+    import threading
+    w, s = make(512, 1024)
+    lin = Linear(w, s)
+    xs = [rows(t, 1024, t) for t in (20, 300)]
+    want = [lin.forward(x) for x in xs]
+    ws, outs, graphs = lin.workspace(300), [torch.empty_like(o) for o in want], []
+    for x, o in zip(xs, outs):
+        lin.forward(x, out=o, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            lin.forward(x, out=o, workspace=ws)
+    for rep in range(3):
+        for o in outs:
+            o.zero_()
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = lin.forward(xs[i])
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(got, want[i]):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i % 2,)) for i in range(4)]
+    [x.start() for x in threads], [x.join() for x in threads]
+    assert not bad
+
+
 @pytest.mark.parametrize("t", [1, 48, 600])
 def test_graph_replays_match_eager(t):
     w, s = make(512, 1024)
@@ -293,6 +352,9 @@ def test_no_tokens_and_refusals():
                  dict(workspace=torch.empty(1 << 16, dtype=torch.uint8))):
         with pytest.raises(ValueError):
             lin.forward(x, **over)
+    square = Linear(*make(256, 256))
+    with pytest.raises(MoeQuantError):
+        square.forward(x, out=x)
     with pytest.raises(MoeQuantError):
         lin.forward(x, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(MoeQuantError):

@@ -12,6 +12,9 @@ using mq::kMaxTokens;
 namespace {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct LinearWs {
@@ -139,6 +142,11 @@ mq_status moe_quant_linear(const mq_linear *l, const uint16_t *x_bf16, const uin
   const bool bf16 = l->out_dtype == MQ_BF16;
   if (!aligned(x_bf16, 16) || !aligned(out, bf16 ? 2 : 4) || (residual_bf16 && !aligned(residual_bf16, 2)))
     return fail(MQ_E_ALIGN, "linear: x must be 16-byte aligned, out and residual to their element");
+  const size_t values = (size_t)num_tokens * l->n;
+  if (overlap(out, values * (bf16 ? 2 : 4), x_bf16, (size_t)num_tokens * l->k * 2))
+    return fail(MQ_E_SHAPE, "linear: out must not overlap x, which other workgroups still read");
+  if (residual_bf16 && (bf16 ? out != residual_bf16 : true) && overlap(out, values * (bf16 ? 2 : 4), residual_bf16, values * 2))
+    return fail(MQ_E_SHAPE, "linear: out may overlap the residual only as a BF16 out that is the residual itself");
   if (!workspace) return fail(MQ_E_WORKSPACE, "linear: workspace is NULL");
   if (!aligned(workspace, 256)) return fail(MQ_E_ALIGN, "linear: workspace not 256-byte aligned");
   const LinearWs w = linear_ws(num_tokens, l->k);
@@ -186,6 +194,11 @@ mq_status moe_quant_kv_append(const mq_kv_cache *c, const mq_rotary *r, int32_t 
     return fail(MQ_E_ALIGN, "kv_append: token strides must be multiples of 8 values");
   if (q && q_out == q && q_stride != q_heads * D)
     return fail(MQ_E_SHAPE, "kv_append: q_out may be q only where q's tokens lie one behind the other");
+  auto span = [&](int64_t stride, int64_t row) { return (size_t)((num_tokens - 1) * stride + row) * 2; };
+  const size_t out_bytes = (size_t)(num_tokens * q_heads * D) * 2;
+  if (q && (overlap(q_out, out_bytes, k, span(k_stride, kv)) || overlap(q_out, out_bytes, v, span(v_stride, kv)) ||
+            (q_out != q && overlap(q_out, out_bytes, q, span(q_stride, q_heads * D)))))
+    return fail(MQ_E_SHAPE, "kv_append: q_out may be q itself but must not overlap q, k and v otherwise");
   mq::KvAppendArgs a;
   a.q = q; a.k = k; a.v = v;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
@@ -238,6 +251,9 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
   if (!aligned(q_bf16, 16) || !aligned(out_bf16, 16) || !aligned(block_table, 4) || !aligned(lengths, 4) ||
       (lse && !aligned(lse, 4)))
     return fail(MQ_E_ALIGN, "attend: q and out must be 16-byte, block_table, lengths and lse 4-byte aligned");
+  const size_t q_bytes = (size_t)(batch * q_heads) * c->head_dim * 2;
+  if (out_bf16 != q_bf16 && overlap(out_bf16, q_bytes, q_bf16, q_bytes))
+    return fail(MQ_E_SHAPE, "attend: out may be q itself but must not overlap it otherwise");
   if (!workspace) return fail(MQ_E_WORKSPACE, "attend: workspace is NULL");
   if (!aligned(workspace, 256)) return fail(MQ_E_ALIGN, "attend: workspace not 256-byte aligned");
   const size_t need = mq::attend_workspace(batch, q_heads, c->kv_heads, c->head_dim);
