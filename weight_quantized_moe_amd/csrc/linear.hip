@@ -35,6 +35,7 @@ namespace {
 
 typedef int i8v __attribute__((ext_vector_type(8)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 // 16-byte values at any even address (rows of an odd number of values)
 typedef u4 u4_a2 __attribute__((aligned(2)));
 
@@ -129,6 +130,15 @@ __global__ __launch_bounds__(256) void linear_quant_kernel(LinearArgs a) {
   }
 }
 
+// To nearest even by the conversion instruction: a tile's 128 values a lane cost 64 of
+// them where the rounding written out takes ten a value, 4 us of a tile of 256 x 256.
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  b2 v;
+  v[0] = (__bf16)a;
+  v[1] = (__bf16)b;
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 // out[t, n .. n + W) = round(y + residual); fast: all W there and rows 16-byte aligned
 template <int W>
 __device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, const float *y, bool fast) {
@@ -151,7 +161,7 @@ __device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, con
         u4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          o[i] = (uint32_t)f32_to_bf16_rne(v[2 * i]) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1]) << 16);
+          o[i] = bf16x2(v[2 * i], v[2 * i + 1]);
         *(u4 *)((uint16_t *)a.out + at + w) = o;
       } else {
         *(f4 *)((float *)a.out + at + w) = f4{v[0], v[1], v[2], v[3]};
@@ -166,7 +176,7 @@ __device__ __forceinline__ void store(const LinearArgs &a, int64_t t, int n, con
     float v = y[i];
     if (a.residual) v += bf16_to_f32(a.residual[at + i]);
     if (a.out_bf16)
-      ((uint16_t *)a.out)[at + i] = f32_to_bf16_rne(v);
+      ((uint16_t *)a.out)[at + i] = (uint16_t)bf16x2(v, v);
     else
       ((float *)a.out)[at + i] = v;
   }
@@ -294,14 +304,15 @@ __global__ __launch_bounds__(64 * kStreamWaves) void linear_stream_kernel(Linear
 // bytes each) and BM activation scales, copied from global memory straight into
 // one of kStages stages of LDS, kStages - 1 steps ahead; one barrier a step.
 //
-// A wave's 64 weight rows are dealt to its 4 results so that a lane ends up with 16
-// consecutive ones: row rho of result j is weight row 16 (rho / 4) + 4 j + rho % 4, so
-// lane group g (rho / 4 in the result's rows) holds rows 16 g + 4 j + i.  A lane then
-// stores 32 bytes of a token's row and four lanes a line of 128.
+// A wave's 64 weight rows are dealt to its 4 results so that a lane ends up with 8
+// consecutive ones in a pair of results: row rho of result j is weight row 32 (j / 2) +
+// 8 (rho / 4) + 4 (j % 2) + rho % 4, so lane group g (rho / 4 in the result's rows) holds
+// 8 g + [0, 8) of each half.  A lane then stores 16 bytes of a token's row and four
+// lanes 64 that lie side by side.
 //
 // LDS: chunk c (16 bytes) of row r lies at slot 8 r + (c ^ swz(r)); the 16 rows that
 // 16 lanes read at once are consecutive for the tokens (swz = r / 2) and rho's above
-// for the weights (swz = 2 (r / 16) + r / 2 % 2), 16 different of 2 x 8 slots either way.
+// for the weights (swz = 2 (r / 8) + r / 2 % 2), 16 different of 2 x 8 slots either way.
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ void dma16(const void *g, unsigned char *lds) {
   __builtin_amdgcn_global_load_lds(g, (lds_void *)lds, 16, 0, 0);
@@ -368,7 +379,7 @@ void linear_tiles_kernel(LinearArgs a) {
   }
   auto wchunk = [&](int p) {
     const int row = 8 * (CW * wave + p) + (lane >> 3);
-    return 16 * ((lane & 7) ^ (2 * ((row >> 4) & 3) + ((row >> 1) & 1)));
+    return 16 * ((lane & 7) ^ (2 * ((row >> 3) & 3) + ((row >> 1) & 1)));
   };
 #pragma unroll
   for (int p = 0; p < CW; ++p)
@@ -401,7 +412,7 @@ void linear_tiles_kernel(LinearArgs a) {
   // ---- the wave's part of the tile
   const int wm = wave / WN, wn = wave - wm * WN;
   const int tok = wm * TM * 16 + r;                                   // + 16 m
-  const int wrow = wn * 64 + 16 * (r >> 2) + (r & 3);                 // + 4 j
+  const int wrow = wn * 64 + 8 * (r >> 2) + (r & 3);                  // + 32 (j / 2) + 4 (j % 2)
   const int blk = (wn * 64) / 128;
   f4 acc[TM][4];
 #pragma unroll
@@ -425,7 +436,7 @@ void linear_tiles_kernel(LinearArgs a) {
     token(0, b[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = wrow + 4 * j, z = 2 * ((n >> 4) & 3) + ((n >> 1) & 1);
+      const int n = wrow + 32 * (j >> 1) + 4 * (j & 1), z = 2 * ((n >> 3) & 3) + ((n >> 1) & 1);
       w[j].set(*(const u4 *)(ws + n * 128 + 16 * (q ^ z)), *(const u4 *)(ws + n * 128 + 16 * ((q + 4) ^ z)));
     }
 #pragma unroll
@@ -490,20 +501,23 @@ void linear_tiles_kernel(LinearArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][j] += sums[((o * L::kWaves + wave) * TM * 4 + 4 * m + j) * 64 + lane];
   }
-  // ---- results: token tok + 16 m, weight rows 64 wn + 16 q + [0, 16)
-  const int n = n0 + wn * 64 + 16 * q;
-  if (n >= a.N) return;
-  const bool fast = n + 16 <= a.N && a.N % 8 == 0 && ((uintptr_t)a.out & 15) == 0;
+  // ---- results: token tok + 16 m, weight rows 64 wn + 32 h + 8 q + [0, 8)
+  const bool rows16 = a.N % 8 == 0 && ((uintptr_t)a.out & 15) == 0;
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
     const int64_t t = t0 + tok + 16 * m;
     if (t >= a.T) continue;
-    float y[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int h = 0; h < 2; ++h) {
+      const int n = n0 + wn * 64 + 32 * h + 8 * q;
+      float y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[4 * j + i] = acc[m][j][i];
-    store<16>(a, t, n, y, fast);
+      for (int i = 0; i < 4; ++i) {
+        y[i] = acc[m][2 * h][i];
+        y[4 + i] = acc[m][2 * h + 1][i];
+      }
+      store<8>(a, t, n, y, rows16 && n + 8 <= a.N);
+    }
   }
 }
 
@@ -549,14 +563,14 @@ hipError_t run_linear(const LinearArgs &a, hipStream_t s) {
     if (cover(16, 32) >= 150) return run_stream<kExact, 2, 1, 2, false>(a, s);
     return run_stream<kExact, 1, 1, 2, false>(a, s);
   }
-  // 256 x 256, a workgroup a CU: four rounds of them at least (16384 x 5120: 205, in
-  // tiles of 128 x 128 221; 4096 x 5120, 1.25 rounds: 78 and 62).  Its registers do not
-  // hold the FP16 operands.
+  // 256 x 256, a workgroup a CU: two rounds of them at least (16384 x 5120: 196, in
+  // tiles of 128 x 128 218; 8192 x 5120, 2.5 rounds: 107 and 109; 4096 x 5120, 1.25: 71
+  // and 59).  Its registers do not hold the FP16 operands.
   if constexpr (!kExact) {
-    if (cover(256, 256) >= 1024) return run_tiles<false, 2, 4, 8, 2>(a, s);
+    if (cover(256, 256) >= 512) return run_tiles<false, 2, 4, 8, 2>(a, s);
   }
-  // 128 x 128 and 64 x 128, two a CU (1024 x 5120, 320 and 640 of them: 26.5 and 28.4;
-  // 2048 x 2048, 256 and 512: 23.8 and 21.6)
+  // 128 x 128 and 64 x 128, two a CU (1024 x 5120, 320 and 640 of them: 24.7 and 27.1;
+  // 2048 x 2048, 256 and 512: 22.1 and 21.3)
   if (cover(128, 128) >= 320) return run_tiles<kExact, 2, 2, 4, 2>(a, s);
   if (cover(64, 128) >= 512) return run_tiles<kExact, 2, 2, 2, 3>(a, s);
   // 64 x 64: two a CU where there are more than CUs (256 x 5120, 320 of them: 13.7), else
