@@ -420,70 +420,78 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_pieces_kernel(AttendArg
           k == 1 ? nullptr : part);
 }
 
-// ---- the pieces of a unit joined, a workgroup per query head: 64 pairs of D (or
-// more, in turn) on each of 4 waves, every wave a fourth of the pieces.  The first
-// pieces' values are asked for together with the maxima and sums.
+// ---- the pieces of a unit joined: a query head to W of a workgroup's 4 waves, a pair
+// of D (or more, in turn) to a lane, every W-th piece to a wave.  W = 4 where there are
+// few units, which then have many pieces, else 1.  The first pieces' values are asked
+// for together with the maxima and sums.
 constexpr int kGroupsMost = 1024;   // of a plan, so no unit has more pieces
 constexpr int kAhead = 8;
 
+template <int W>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan plan) {
-  __shared__ float sx[4][64], sy[4][64], weight[kGroupsMost];
+  __shared__ float sx[4][64], sy[4][64], weight[4 / W][kGroupsMost];
   const int units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
-  const int b = blockIdx.x / units, kt = blockIdx.x - b * units, r = blockIdx.y;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = a.D, mine = wave / W, first = wave % W;
+  const int b = blockIdx.x / units, kt = blockIdx.x - b * units, r = blockIdx.y * (4 / W) + mine;
   const int f0 = plan.first[b], k = (plan.first[b + 1] - f0) / units;
   const Heads h = heads_of(a, b, kt);
-  if (k <= 1 || r >= h.nh) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = a.D;
+  if (k <= 1) return;
+  const bool live = r < h.nh;       // (of W = 1 some of the last workgroup's waves are not)
+  if (W == 4 && !live) return;
   const int64_t size = part_size(a);
   const int R = rows_of(a);
   const float *part = plan.parts + (f0 + kt * k) * size;
-  float2 ahead[kAhead];
   auto values = [&](int w, int d) { return *(const float2 *)(part + w * size + 2 * R + r * D + d); };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    ahead[i] = float2{0.f, 0.f};
-    if (wave + 4 * i < k && 2 * lane < D) ahead[i] = values(wave + 4 * i, 2 * lane);
-  }
+  float2 ahead[kAhead];
   float m = -INFINITY, l = 0.f;
-  for (int w = lane; w < k; w += 64) m = fmaxf(m, part[w * size + r]);
+  if (live) {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
-  const float mm = m == -INFINITY ? 0.f : m;
-  for (int w = lane; w < k; w += 64) {
-    const float f = __builtin_amdgcn_exp2f(part[w * size + r] - mm);
-    l += part[w * size + R + r] * f;
-    if (wave == 0) weight[w] = f;
+    for (int i = 0; i < kAhead; ++i) {
+      ahead[i] = float2{0.f, 0.f};
+      if (first + W * i < k && 2 * lane < D) ahead[i] = values(first + W * i, 2 * lane);
+    }
+    for (int w = lane; w < k; w += 64) m = fmaxf(m, part[w * size + r]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
+    const float mm = m == -INFINITY ? 0.f : m;
+    for (int w = lane; w < k; w += 64) {
+      const float f = __builtin_amdgcn_exp2f(part[w * size + r] - mm);
+      l += part[w * size + R + r] * f;
+      if (first == 0) weight[mine][w] = f;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, 64);
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d, 64);
   __syncthreads();
   for (int d0 = 0; d0 < D; d0 += 128) {
     const int d = d0 + 2 * lane;
     float x = 0.f, y = 0.f;
-    if (d < D) {
+    if (live && d < D) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int w = wave + 4 * i;
+        const int w = first + W * i;
         if (w < k) {
           const float2 o = d0 ? values(w, d) : ahead[i];
-          x += weight[w] * o.x;
-          y += weight[w] * o.y;
+          x += weight[mine][w] * o.x;
+          y += weight[mine][w] * o.y;
         }
       }
 #pragma unroll 4
-      for (int w = wave + 4 * kAhead; w < k; w += 4) {
+      for (int w = first + W * kAhead; w < k; w += W) {
         const float2 o = values(w, d);
-        x += weight[w] * o.x;
-        y += weight[w] * o.y;
+        x += weight[mine][w] * o.x;
+        y += weight[mine][w] * o.y;
       }
     }
-    __syncthreads();
-    sx[wave][lane] = x;
-    sy[wave][lane] = y;
-    __syncthreads();
-    if (wave == 0 && d < D)
-      Attend<64, false>::write_out(a, h.head + r, d, m, l, (sx[0][lane] + sx[1][lane]) + (sx[2][lane] + sx[3][lane]),
-                                   (sy[0][lane] + sy[1][lane]) + (sy[2][lane] + sy[3][lane]));
+    if constexpr (W == 4) {
+      __syncthreads();
+      sx[wave][lane] = x;
+      sy[wave][lane] = y;
+      __syncthreads();
+      x = (sx[0][lane] + sx[1][lane]) + (sx[2][lane] + sx[3][lane]);
+      y = (sy[0][lane] + sy[1][lane]) + (sy[2][lane] + sy[3][lane]);
+    }
+    if (first == 0 && live && d < D) Attend<64, false>::write_out(a, h.head + r, d, m, l, x, y);
   }
 }
 
@@ -527,7 +535,11 @@ static hipError_t run_attend(const AttendArgs &a, hipStream_t s) {
   }
   const Plan plan = {groups, share_min, (int *)a.ws, (float *)((char *)a.ws + first_bytes(a.B))};
   attend_pieces_kernel<DT, FP8><<<dim3(groups + units), dim3(64 * kWaves), 0, s>>>(a, plan);
-  attend_join_kernel<<<dim3(units, G < 16 ? G : 16), dim3(256), 0, s>>>(a, plan);
+  const unsigned heads = G < 16 ? G : 16;
+  if (units <= 64)
+    attend_join_kernel<4><<<dim3(units, heads), dim3(256), 0, s>>>(a, plan);
+  else
+    attend_join_kernel<1><<<dim3(units, (heads + 3) / 4), dim3(256), 0, s>>>(a, plan);
   return hipGetLastError();
 }
 

@@ -10,12 +10,12 @@
 // (exact) and go through four 16x16x32 FP16 instructions, whose sums are FP32
 // ones (2^-23.7 of the largest product in the mean), at half the rate.
 //
-// For many tokens bound by instructions: at 8192^3 the 256 x 256 tiles run at 2070
+// For many tokens bound by instructions: at 8192^3 the 256 x 256 tiles run at 2260
 // TFLOP/s (the quantization aside), with the matrix units busy half of the cycles
-// and the vector units 41%, mostly the four scaling sums per matrix instruction;
-// without those it is 13% faster, without the copies into LDS 20%, and the library's
-// product of E4M3 tensors with one scale each reaches 2716.  16384 x 5120 x 2048: 190 us
-// (1810 TFLOP/s), the tiles' starts and ends being 15% of it, after 22 us for the
+// and the vector units 41%, mostly the four scaling sums per matrix instruction (a copy
+// without those ran 13% faster, one without the copies into LDS 20%); the library's
+// product of E4M3 tensors with one scale each reaches 2716.  16384 x 5120 x 2048: 178 us
+// (1930 TFLOP/s), about a tenth of it the tiles' starts and ends, after 21 us for the
 // quantization (100 MB).  For few tokens bound by launches and latency.
 //
 // Three ways through it:
