@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_units_kernel(AttendArgs
 // evenly to `groups`.  The lengths are known on the device only: every wave of a
 // workgroup x goes through them (64 a step) for the piece that is number x, and
 // the pieces behind the last one, at most groups + units in all, have nothing to do.
-__device__ __forceinline__ int wave_sum(int v) {
+__device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
   return v;
@@ -384,9 +384,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_pieces_kernel(AttendArg
   const int lane = threadIdx.x & 63, units = a.Hk * ((a.Hq / a.Hk + 15) / 16);
   auto tiles_of = [&](int b) { return b < a.B ? span_of(a, a.lengths[b]).tiles : 0; };
   int64_t total = 0;
-  for (int b = 0; b < a.B; b += 64) total += wave_sum(tiles_of(b + lane));
+  for (int b = 0; b < a.B; b += 64) total += wave_sum((uint32_t)tiles_of(b + lane));  // 64 of at most 2^25
   total *= units;
-  const int share = (int)max((int64_t)plan.share_min, (total + plan.groups - 1) / plan.groups);
+  // (a share above a request's 2^25 tiles is as good as any)
+  const int share = (int)min((int64_t)1 << 26, max((int64_t)plan.share_min, (total + plan.groups - 1) / plan.groups));
   int base = 0, found = -1, rel = 0, k = 1;
   for (int b = 0; b < a.B; b += 64) {
     const int n = tiles_of(b + lane), mine = b + lane < a.B ? max(1, (n + share - 1) / share) : 0;
