@@ -579,9 +579,9 @@ typedef struct {
  *               cos_sin, is padding: nothing of it is written
  *   q_out       [T, q_heads, D] BF16 bits, 16-byte aligned; may be q itself where
  *               q_stride is q_heads * D, and does not overlap q, k and v otherwise
- * MQ_KV_FP8 keeps RNE-to-E4M3(value / scale), saturated to +-448.  The slots of
- * one call are distinct: of a slot given twice it is unspecified which token's
- * values stay, per 8 values.
+ * MQ_KV_FP8 keeps RNE-to-E4M3(value / scale), one IEEE FP32 division, saturated to
+ * +-448.  The slots of one call are distinct: of a slot given twice it is
+ * unspecified which token's values stay, per 8 values.
  * num_tokens == 0 returns MQ_OK without enqueuing anything.
  * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE, MQ_E_DTYPE, MQ_E_ALIGN, MQ_E_HIP.
  */

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import attention as oattn
+from oracle import codecs
 from weight_quantized_moe_amd import KVCache, MoeQuantError, Rotary
 
 pytestmark = pytest.mark.gpu
@@ -284,3 +285,26 @@ def _in_place(c):
                                           c.k.stride(0), c.v.data_ptr(), c.v.stride(0), c.positions.data_ptr(),
                                           c.slots.data_ptr(), 8, c.q.data_ptr(), None)
     binding._check(c.cache._lib, st)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -149, 1e-42, 1e-40, 2.0 ** -128, 3e-39, 2.0 ** -126, 1e-36, 1e-27, 2.0 ** -9, 0.7,
+                                   1.9999999, 1e20, 2.0 ** 126, 2.0 ** 127, 3.4e38])
+def test_codes_of_scales_of_every_size(scale):
+    """RNE-to-E4M3 of one FP32 division, bit for bit: zeros, values of every code, ties and
+    what saturates, also where the scale's reciprocal is infinite or subnormal."""
+    gen, s = torch.Generator().manual_seed(11), np.float32(scale)
+    steps = torch.randn(40, 4, 64, generator=gen) * torch.exp2(torch.randint(-12, 10, (40, 4, 64), generator=gen))
+    steps[10:25] = torch.randint(-470, 471, (15, 4, 64), generator=gen).float()
+    steps[30:33] = 0
+    x = (steps.double() * float(s)).clamp(-3e38, 3e38).float().to(BF)
+    c = Case(40, 2, 2, 64, 0, 16, E4, norm=False, ks=scale, vs=scale)
+    c.k, c.v = x[:, :2].contiguous().cuda(), x[:, 2:].contiguous().cuda()
+    c.cache.append(c.rotary, None, c.k, c.v, None, c.slots)
+    torch.cuda.synchronize()
+    at = c.slots.long().cpu()
+    for cache, new in ((c.kc, x[:, :2]), (c.vc, x[:, 2:])):
+        got = bits(cache).cpu()[at // 16, :, at % 16].numpy()
+        with np.errstate(over="ignore"):
+            want = codecs.quantize_e4m3((new.float().numpy() / s).astype(np.float64))
+        assert np.array_equal(got & 127, want & 127), np.argwhere((got ^ want) & 127)[:4]
+        assert np.array_equal((got >> 7)[want & 127 > 0], (want >> 7)[want & 127 > 0])

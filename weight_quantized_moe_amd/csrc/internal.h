@@ -209,6 +209,7 @@ struct KvAppendArgs {
   int64_t num_slots, T;
   int Hq, Hk, D, R, interleaved, max_positions, page_log2, fp8;
   float eps, k_scale, v_scale;
+  float k_inv, v_inv;   // set by the launch
 };
 constexpr int kMaxHeads = 1024;
 constexpr int64_t kMaxBatch = 1 << 16;     // requests of one attention

@@ -50,18 +50,30 @@ __device__ __forceinline__ u4 narrow8(const float *f) {
   return o;
 }
 // v / s saturated to +-448, NaN kept: the rounded reciprocal y's quotient corrected by
-// its remainder, within the FP32 rounding of v / s
+// its remainder, which is v / s rounded (see quotient_by)
 __device__ __forceinline__ float saturated(float v, float s, float y) {
   const float q = v * y, c = __builtin_fmaf(__builtin_fmaf(-q, s, v), y, q);
   const float w = fabsf(q) < 500.f ? c : q;
   return w != w ? w : __builtin_amdgcn_fmed3f(w, -448.f, 448.f);
 }
+// y: quotient_by(s)
 __device__ __forceinline__ u2 codes8(const float *f, float s, float y) {
+  float v[8];
+  if (y != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = saturated(f[i], s, y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = f[i] / s;
+      v[i] = w != w ? w : __builtin_amdgcn_fmed3f(w, -448.f, 448.f);
+    }
+  }
   u2 o;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(saturated(f[4 * i], s, y), saturated(f[4 * i + 1], s, y), 0, false);
-    o[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(saturated(f[4 * i + 2], s, y), saturated(f[4 * i + 3], s, y), w, true);
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+    o[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], w, true);
   }
   return o;
 }
@@ -175,7 +187,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int part
       const int64_t o = (((page * a.Hk + kh) << a.page_log2) + at) * a.D;
       void *cache = kind == 1 ? a.kc : a.vc;
       if constexpr (FP8) {
-        const float sc = kind == 1 ? a.k_scale : a.v_scale, y = 1.f / sc;
+        const float sc = kind == 1 ? a.k_scale : a.v_scale, y = kind == 1 ? a.k_inv : a.v_inv;
         *(u2 *)((uint8_t *)cache + o + ia) = codes8(xa, sc, y);
         *(u2 *)((uint8_t *)cache + o + ib) = codes8(xb, sc, y);
       } else {
@@ -202,7 +214,19 @@ void run_append(const KvAppendArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s) {
+// The rounded 1 / s where a quotient v / s follows from it (Markstein's theorem), 0 where
+// the kernel has to divide: for a reciprocal that is infinite or subnormal, a remainder
+// of a quotient that has a code (2^-11 s at least) below 2^-149, and a mantissa of s of
+// all ones.
+static float quotient_by(float s) {
+  if (!(s >= 0x1p-90f && s <= 0x1p126f) || (__builtin_bit_cast(uint32_t, s) & 0x7FFFFFu) == 0x7FFFFFu) return 0.f;
+  return 1.f / s;
+}
+
+hipError_t launch_kv_append(const KvAppendArgs &args, hipStream_t s) {
+  KvAppendArgs a = args;
+  a.k_inv = quotient_by(a.k_scale);
+  a.v_inv = quotient_by(a.v_scale);
   if (a.D <= 16) run_append<1>(a, s);
   else if (a.D <= 32) run_append<2>(a, s);
   else if (a.D <= 64) run_append<4>(a, s);
