@@ -547,7 +547,8 @@ typedef struct {
 /*
  * What happens to a head's query and key before attention, in FP32 and rounded
  * once at the end:
- *   h = x,  or with a norm weight  x / sqrt(mean(x^2) + eps) * weight   (mean over D);
+ *   h = x,  or with a norm weight  x / sqrt(mean(x^2) + eps) * weight   (mean over D,
+ *   finite values of any size);
  *   the first rot_dim values of h are turned by the angles of the token's
  *   position, in pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved:
  *     (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i).

@@ -308,3 +308,20 @@ def test_codes_of_scales_of_every_size(scale):
             want = codecs.quantize_e4m3((new.float().numpy() / s).astype(np.float64))
         assert np.array_equal(got & 127, want & 127), np.argwhere((got ^ want) & 127)[:4]
         assert np.array_equal((got >> 7)[want & 127 > 0], (want >> 7)[want & 127 > 0])
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("d,r", [(16, 16), (64, 64), (96, 0), (128, 64), (256, 256)])
+def test_norms_of_large_heads(d, r, dtype):
+    """Heads whose squares add up beyond FP32's range, beside ordinary ones and zeros."""
+    for size in (2.0 ** 59, 1e19, 1e25, 5e37):
+        for inter in (False, True):
+            c = Case(21, 5, 3, d, r, 16, dtype, inter, fused=False, seed=d, size=size)
+            gen = torch.Generator(device="cuda").manual_seed(1)
+            for x in (c.q, c.k):
+                x[3] = randn(gen, *x[3].shape).to(BF)
+                x[4, 0] = 0
+                x[5, 1] = torch.finfo(BF).max
+                x[6, :, 1:] = 0
+                x[7, 0] *= 2.0 ** -60
+            c.check()

@@ -142,13 +142,29 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, int part
     const int kind = h < a.Hq ? 0 : h < a.Hq + a.Hk ? 1 : 2;
     const bool norm = kind == 0 ? a.q_norm != nullptr : kind == 1 && a.k_norm != nullptr;
     if (__any(norm)) {
-      float sum = 0.f;
+      auto squares = [&]() {
+        float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += xa[i] * xa[i] + xb[i] * xb[i];
+        for (int i = 0; i < 8; ++i) sum += xa[i] * xa[i] + xb[i] * xb[i];
 #pragma unroll
-      for (int d = 1; d < LP; d *= 2) sum += __shfl_xor(sum, d, 64);
+        for (int d = 1; d < LP; d *= 2) sum += __shfl_xor(sum, d, 64);
+        return sum;
+      };
+      float sum = squares(), eps = a.eps;
+      const bool large = norm && sum == INFINITY;
+      if (__any(large)) {
+        // values of 2^60 or more: 2^-70 of the head has the same norm, and squares in range
+        const float k = large ? 0x1p-70f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          xa[i] *= k;
+          xb[i] *= k;
+        }
+        sum = squares();
+        eps *= k * k;
+      }
       if (norm) {
-        const float f = 1.f / sqrtf(sum / (float)a.D + a.eps);
+        const float f = 1.f / sqrtf(sum / (float)a.D + eps);
         float w[8];
         widen8(kind ? wk[0] : wq[0], w);
 #pragma unroll
