@@ -319,3 +319,23 @@ def test_no_requests_and_refusals():
     for over in (dict(window=-1), dict(scale=math.nan), dict(q=c.q[:, :7].contiguous())):
         with pytest.raises(MoeQuantError):
             c.cache.attend(**dict(good, **over))
+
+
+@pytest.mark.parametrize("n,scale", [(300, 1e-42), (300, 1e-39), (1 << 18, 1e-39), (1 << 18, 1e-38), (1 << 18, 2.0 ** -100),
+                                     (1 << 18, 1e35)])
+def test_value_scales_of_every_size(n, scale):
+    """Every token the same value, so that is the result, however many there are: the
+    sums of equal terms are off by (n / 16 + 96) 2^-24 at most and mostly exact, the
+    quotient and the scale's product by a rounding each; then half a step."""
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    pages = -(-n // 1024)
+    k, v = (torch.zeros(pages, 1, 1024, 64, dtype=E4, device="cuda") for _ in range(2))
+    row = (200.0 * torch.randn(64, generator=gen, device="cuda")).clamp(-448, 448).to(E4)
+    v[:] = row
+    q = torch.randn(1, 3, 64, generator=gen, device="cuda").to(BF)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    out = KVCache(k, v, v_scale=scale).attend(q, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    ref = f64(row) * float(np.float32(scale))
+    lim = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -6) + 2.0 ** -134
+    assert np.all(np.abs(f64(out[0]) - ref) <= lim), float((np.abs(f64(out[0]) - ref) / lim).max())

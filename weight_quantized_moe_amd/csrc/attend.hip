@@ -316,8 +316,9 @@ struct Attend {
 
   // Two values of head hd's result from its maximum, sum and O.
   static __device__ __forceinline__ void write_out(const AttendArgs &a, int64_t hd, int d, float m, float l, float x, float y) {
-    const float f = l > 0.f ? a.v_scale / l : 0.f;
-    *(uint32_t *)(a.out + hd * a.D + d) = pack_bf16(x * f, y * f);
+    // (v_scale / l may be subnormal: the scale comes last)
+    const float f = l > 0.f ? 1.f / l : 0.f;
+    *(uint32_t *)(a.out + hd * a.D + d) = pack_bf16(x * f * a.v_scale, y * f * a.v_scale);
     if (a.lse && d == 0) a.lse[hd] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
   }
 };
