@@ -339,3 +339,19 @@ def test_value_scales_of_every_size(n, scale):
     ref = f64(row) * float(np.float32(scale))
     lim = 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -6) + 2.0 ** -134
     assert np.all(np.abs(f64(out[0]) - ref) <= lim), float((np.abs(f64(out[0]) - ref) / lim).max())
+
+
+def test_a_nan_query_shows_in_both_results():
+    """In its own head alone, in one launch and in two."""
+    for lengths in ([40, 20, 3], [700, 9000, 3]):
+        c = Case(lengths, 8, 2, 128, seed=19)
+        want, lse = (x.clone() for x in c.check())
+        for b, h in ((0, 1), (1, 6)):
+            q = c.q.clone()
+            q[b, h, 17] = math.nan
+            l2 = torch.empty_like(lse)
+            got = c.cache.attend(q, c.table, c.lengths, lse=l2)
+            torch.cuda.synchronize()
+            assert torch.isnan(got[b, h]).all() and torch.isnan(l2[b, h])
+            got[b, h], l2[b, h] = want[b, h], lse[b, h]
+            assert torch.equal(got, want) and torch.equal(l2, lse)

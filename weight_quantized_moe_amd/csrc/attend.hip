@@ -316,10 +316,11 @@ struct Attend {
 
   // Two values of head hd's result from its maximum, sum and O.
   static __device__ __forceinline__ void write_out(const AttendArgs &a, int64_t hd, int d, float m, float l, float x, float y) {
+    // l: 0 only where no token is there, else 1 at least, or NaN for a query of NaN.
     // (v_scale / l may be subnormal: the scale comes last)
-    const float f = l > 0.f ? 1.f / l : 0.f;
+    const float f = l == 0.f ? 0.f : 1.f / l;
     *(uint32_t *)(a.out + hd * a.D + d) = pack_bf16(x * f * a.v_scale, y * f * a.v_scale);
-    if (a.lse && d == 0) a.lse[hd] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+    if (a.lse && d == 0) a.lse[hd] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
   }
 };
 
