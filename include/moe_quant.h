@@ -623,8 +623,10 @@ mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads,
  * queries, keys and values of the tokens themselves are finite.  Repeated calls
  * give the same bits.  batch == 0 returns MQ_OK without enqueuing anything.
  * Limits: batch at most 65536, batch * kv_heads * ceil(q_heads / kv_heads / 16) at
- * most 2^23; q_heads a multiple of kv_heads, at most 1024; scale and scale * k_scale finite; window 0 (none) or positive; max_pages *
- * page_size at most 2^30.
+ * most 2^23; q_heads a multiple of kv_heads, at most 1024; scale * k_scale * log2(e)
+ * finite; window 0 (none) or positive; max_pages * page_size at most 2^30.  Scores
+ * times log2(e), and the sums of exp(s_j - max s) |v_j| of the stored values, are below
+ * FP32's largest number, 2^128.
  * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE, MQ_E_DTYPE, MQ_E_ALIGN,
  * MQ_E_WORKSPACE, MQ_E_HIP.
  */

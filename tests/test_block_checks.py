@@ -275,3 +275,12 @@ def test_oracle_attend_on_a_dense_cache():
             assert np.isclose(lse[b, h], np.log(e.sum()))
     out, lse, _, _ = oattn.attend(q, k, v, table, [0, -3], 0.25)
     assert not out.any() and np.all(lse == -np.inf)
+
+
+def test_attend_refuses_scales_whose_base_2_factor_is_infinite(lib):
+    """Scores become exponents of 2: scale k_scale log2(e) has to be finite, 2.3586e38 at most."""
+    for dtype, ks, scale, expect in ((0, 1.0, 2.36e38, SHAPE), (0, 1.0, -3e38, SHAPE), (0, 1.0, 2.358e38, WORKSPACE),
+                                     (1, 1e19, 2.4e19, SHAPE), (1, 1e19, 2.3e19, WORKSPACE), (1, 1e-5, 3e38, WORKSPACE)):
+        c = ctypes.byref(_cache(dtype=dtype, ks=ks))
+        got = lib.moe_quant_attend(c, 8, scale, 0, P, P, 7, 7, P, 5, P, None, None, 0, None)
+        assert got == expect, (dtype, ks, scale)

@@ -57,7 +57,7 @@ constexpr int kTile = 32;    // tokens of one step of a wave
 constexpr int kWaves = 4;
 // Requests that the pieces' plan goes through; a workgroup takes whole units above it.
 constexpr int kPlanBatch = 1024;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr float kLn2 = 0.693147180559945309417f;
 
 // Heads of a unit at most, and floats of a part of one: R maxima, R sums, O [R, D].
 __host__ __device__ __forceinline__ int rows_of(const AttendArgs &a) { return a.Hq / a.Hk < 16 ? a.Hq / a.Hk : 16; }
@@ -246,7 +246,7 @@ struct Attend {
 #pragma unroll
     for (int j = 0; j < VJ; ++j) R.o[j] = f4{0.f, 0.f, 0.f, 0.f};
     const int32_t *table = a.table + b * a.table_stride;
-    const float c = a.score_scale * kLog2e;
+    const float c = a.score_scale;
     // one tile's loads are in flight while the one before is computed, and the page
     // numbers of the tile after that
     const int base = (start / kTile) * kTile, step = kWaves * kTile, stop = base + t1 * kTile;

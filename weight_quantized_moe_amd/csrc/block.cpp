@@ -236,8 +236,10 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
   if (st == MQ_OK) st = check_batch(batch, "attend");
   if (st == MQ_OK) st = check_units(c, q_heads, batch, "attend");
   if (st != MQ_OK) return st;
-  if (!std::isfinite(scale) || !std::isfinite(scale * c->k_scale))
-    return fail(MQ_E_SHAPE, "attend: scale %g (times k_scale %g) must be finite", (double)scale, (double)c->k_scale);
+  const float score_scale = scale * c->k_scale * 1.44269504088896340736f;
+  if (!std::isfinite(scale) || !std::isfinite(score_scale))
+    return fail(MQ_E_SHAPE, "attend: scale %g, and times k_scale %g and log2(e), must be finite", (double)scale,
+                (double)c->k_scale);
   if (window < 0) return fail(MQ_E_SHAPE, "attend: window %d must not be negative", window);
   if (max_pages < 0 || max_pages > mq::kMaxRequest / c->page_size || table_stride < max_pages)
     return fail(MQ_E_SHAPE, "attend: max_pages %d times page_size must be at most 2^30, table_stride %lld at least "
@@ -264,7 +266,7 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
   a.table_stride = table_stride; a.out = out_bf16; a.lse = lse; a.ws = workspace;
   a.B = (int)batch; a.Hq = q_heads; a.Hk = c->kv_heads; a.D = c->head_dim; a.page_log2 = __builtin_ctz(c->page_size);
   a.num_pages = (int)c->num_pages; a.max_tokens = max_pages * c->page_size; a.window = window;
-  a.score_scale = scale * c->k_scale; a.v_scale = c->v_scale;
+  a.score_scale = score_scale; a.v_scale = c->v_scale;
   const hipError_t e = mq::launch_attend(a, c->dtype == MQ_KV_FP8, (hipStream_t)stream);
   if (e != hipSuccess) return fail(MQ_E_HIP, "attend: %s", hipGetErrorString(e));
   mq::clear_error();

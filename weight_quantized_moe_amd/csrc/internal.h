@@ -226,7 +226,7 @@ struct AttendArgs {
   float *lse;
   void *ws;
   int B, Hq, Hk, D, page_log2, num_pages, max_tokens, window;
-  float score_scale;  // scale * k_scale
+  float score_scale;  // scale * k_scale * log2(e): scores are exponents of 2
   float v_scale;
 };
 size_t attend_workspace(int64_t B, int Hq, int Hk, int D);
