@@ -491,8 +491,8 @@ mq_status moe_quant_norm(const mq_norm *n, const uint16_t *x_bf16, const void *r
  * sums in FP32.  For an FP32 output the products of codes are exact; for a BF16
  * one they come from the FP8 matrix units, which cut the 128 products of a block
  * at 2^-16 of their largest (an error of 6e-5 of it in the mean).  N and K need
- * not fill their last block.  A weight code of NaN (0x7F, 0xFF) makes
- * its output column NaN; x must be finite.
+ * not fill their last block.  A weight code of NaN (0x7F, 0xFF) makes its output
+ * column NaN, a NaN or an infinity in x its output row.
  */
 typedef struct {
   uint32_t abi_version; /* must equal MOE_QUANT_ABI_VERSION                          */

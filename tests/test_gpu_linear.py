@@ -359,3 +359,26 @@ def test_no_tokens_and_refusals():
         lin.forward(x, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(MoeQuantError):
         Linear(*make(128, 264))                                      # no multiple of 16
+
+
+@pytest.mark.parametrize("t,n,k", [(1, 128, 256), (5, 300, 400), (16, 512, 2064), (40, 256, 1040), (64, 4801, 528),
+                                   (130, 4000, 144), (300, 1000, 400), (600, 2000, 400), (2049, 2100, 272), (2050, 2570, 144),
+                                   (8197, 8200, 144)])
+def test_activations_that_are_not_finite_show_in_their_rows(t, n, k):
+    w, s = make(n, k, 3)
+    w[n // 2] = 0                                                    # and where the weights are zero
+    x = rows(t, k, 3)
+    for dtype in (BF, F32):
+        lin = Linear(w, s, out_dtype=dtype)
+        want = lin.forward(x)
+        bad = x.clone()
+        at = sorted({0, t // 2, t - 1})
+        for i, value in zip(at, (float("nan"), float("inf"), -float("inf"))):
+            bad[i, (5, k - 1, 100)[at.index(i)]] = value
+        got = lin.forward(bad)
+        torch.cuda.synchronize()
+        assert torch.isnan(got[at]).all()
+        got[at] = want[at]
+        assert torch.equal(got, want)
+        if t > 3000:
+            break
