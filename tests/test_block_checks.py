@@ -14,6 +14,7 @@ import torch
 from oracle import attention as oattn
 from oracle import codecs
 from oracle import linear as olin
+from oracle import w8a8
 from weight_quantized_moe_amd import KVCache, Linear, MoeQuantError, Rotary, binding, build
 from weight_quantized_moe_amd.binding import KvCacheDesc, LinearDesc, RotaryDesc
 
@@ -284,3 +285,20 @@ def test_attend_refuses_scales_whose_base_2_factor_is_infinite(lib):
         c = ctypes.byref(_cache(dtype=dtype, ks=ks))
         got = lib.moe_quant_attend(c, 8, scale, 0, P, P, 7, 7, P, 5, P, None, None, 0, None)
         assert got == expect, (dtype, ks, scale)
+
+
+def test_how_the_rows_codes_relate_to_the_layers():
+    """The product's scale is m * fl(1 / 448), the layer's m / 448: the same or the next
+    FP32 number, for 71 of a BF16 maximum's 128 mantissas; codes a step apart at most."""
+    m = np.zeros((128, 128), np.float32)
+    m[:, 0] = 1 + np.arange(128) / 128
+    far = olin.quantize_rows(m)[1].view(np.int32) - w8a8.quantize_act(m)[1].view(np.int32)
+    assert int((far == 1).sum()) == 71 and int((far == 0).sum()) == 57
+    x = torch.randn(1000, 512, generator=torch.Generator().manual_seed(0)).bfloat16().float().numpy()
+    (a, sa), (b, sb) = olin.quantize_rows(x), w8a8.quantize_act(x)
+    far = sa.view(np.int32) - sb.view(np.int32)
+    assert np.all((far == 0) | (far == 1))
+    step = (a & 127).astype(int) - (b & 127)
+    assert np.all(np.abs(step) <= 1) and np.array_equal(a >> 7, b >> 7)
+    # and only in blocks whose scales differ
+    assert 1 / 2000 < np.mean(step != 0) < 1 / 400 and not step[np.repeat(far, 128, 1) == 0].any()

@@ -603,7 +603,8 @@ class Linear:
     """A dense projection on E4M3 weights with a scale for each block of 128
     (moe_quant_linear): ``w`` uint8 [N, K] (E4M3FN bits), ``w_scale`` float32
     [ceil(N / 128), ceil(K / 128)], both on the GPU and alive as long as the object.
-    The rows are quantized to E4M3 per 128 values, as in ``Layer.forward_w8a8``.
+    The rows are quantized to E4M3 per 128 values; their scale is a product with
+    1 / 448 where ``Layer.forward_w8a8`` divides, so one code in 900 is not its code.
     ``out_dtype``: bfloat16 (default) or float32."""
 
     def __init__(self, w, w_scale, out_dtype=None):
