@@ -600,8 +600,8 @@ mq_status moe_quant_kv_append(const mq_kv_cache *c, const mq_rotary *r, int32_t 
                               uint16_t *q_out, struct ihipStream_t *stream);
 
 /*
- * Device workspace bytes of moe_quant_attend over a batch of requests, for any
- * lengths (256-byte aligned start required).  Host only.
+ * Device workspace bytes of moe_quant_attend over up to `batch` requests, for any
+ * lengths: never less for more requests (256-byte aligned start required).  Host only.
  */
 mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads, int64_t batch,
                                           size_t *bytes);
@@ -628,7 +628,9 @@ mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads,
  * Tokens on a page outside of [0, num_pages) count as absent.  What the cache
  * holds behind a request's last token, NaN among it, does not reach the result;
  * queries, keys and values of the tokens themselves are finite.  Repeated calls
- * give the same bits.  batch == 0 returns MQ_OK without enqueuing anything.
+ * give the same bits.  Up to 1024 requests are cut into pieces where they are long;
+ * of more, each goes whole to one workgroup per 16 query heads of a key head.
+ * batch == 0 returns MQ_OK without enqueuing anything.
  * Limits: batch at most 65536, batch * kv_heads * ceil(q_heads / kv_heads / 16) at
  * most 2^23; q_heads a multiple of kv_heads, at most 1024; scale * k_scale * log2(e)
  * finite; window 0 (none) or positive; max_pages * page_size at most 2^30.  Scores

@@ -302,3 +302,15 @@ def test_how_the_rows_codes_relate_to_the_layers():
     assert np.all(np.abs(step) <= 1) and np.array_equal(a >> 7, b >> 7)
     # and only in blocks whose scales differ
     assert 1 / 2000 < np.mean(step != 0) < 1 / 400 and not step[np.repeat(far, 128, 1) == 0].any()
+
+
+def test_attend_workspace_does_not_shrink_with_the_batch(lib):
+    """One sized for the largest batch serves every smaller one, across 1024 requests, where
+    the plan of pieces ends, too."""
+    for heads, hq, d in ((1, 1, 16), (1, 20, 128), (4, 32, 128), (8, 8, 64), (16, 256, 256), (64, 64, 80), (1024, 1024, 64)):
+        c, last = ctypes.byref(_cache(heads=heads, d=d)), 0
+        for batch in list(range(0, 140)) + [255, 256, 257, 511, 512, 513, 1023, 1024, 1025, 2048, 8192]:
+            b = ctypes.c_size_t()
+            assert lib.moe_quant_attend_workspace_size(c, hq, batch, ctypes.byref(b)) == OK
+            assert b.value >= last, (heads, hq, d, batch)
+            last = b.value

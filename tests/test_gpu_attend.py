@@ -355,3 +355,15 @@ def test_a_nan_query_shows_in_both_results():
             assert torch.isnan(got[b, h]).all() and torch.isnan(l2[b, h])
             got[b, h], l2[b, h] = want[b, h], lse[b, h]
             assert torch.equal(got, want) and torch.equal(l2, lse)
+
+
+def test_one_workspace_for_every_batch():
+    """Sized for the largest; more than 1024 requests go whole and need 256 bytes of it."""
+    c = Case([100, 9000] + [5] * 1098, 8, 2, 64, seed=21)
+    want, _ = c.check(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    ws = c.cache.attend_workspace(1100, 8)
+    for b in (1100, 1024, 300, 2, 1):
+        got = c.cache.attend(c.q[:b], c.table[:b], c.lengths[:b], workspace=ws)
+        torch.cuda.synchronize()
+        # cut elsewhere: half a step each
+        assert torch.allclose(got.float(), want[:b].float(), rtol=2.0 ** -6, atol=1e-4), b

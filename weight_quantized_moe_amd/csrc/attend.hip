@@ -517,12 +517,18 @@ int share_min_of(int64_t units) { return units / 8 < 4 ? 4 : units / 8 > 128 ? 1
 // [B + 1] numbers of pieces, then the parts.
 static size_t first_bytes(int64_t B) { return ((size_t)(B + 1) * 4 + 255) / 256 * 256; }
 
-size_t attend_workspace(int64_t B, int Hq, int Hk, int D) {
+size_t attend_workspace_need(int64_t B, int Hq, int Hk, int D) {
   if (B > kPlanBatch) return 256;   // no pieces
   AttendArgs a{};
   a.Hq = Hq; a.Hk = Hk; a.D = D;
   const int64_t units = B * Hk * ((Hq / Hk + 15) / 16);
   return first_bytes(B) + ((size_t)(groups_of(units) + units) * part_size(a) * 4 + 255) / 256 * 256;
+}
+
+// What a call of any number of requests up to B needs: groups_of(units) + units and so
+// the need grow with B up to kPlanBatch.
+size_t attend_workspace(int64_t B, int Hq, int Hk, int D) {
+  return attend_workspace_need(B < kPlanBatch ? B : kPlanBatch, Hq, Hk, D);
 }
 
 template <int DT, bool FP8>

@@ -258,7 +258,7 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
     return fail(MQ_E_SHAPE, "attend: out may be q itself but must not overlap it otherwise");
   if (!workspace) return fail(MQ_E_WORKSPACE, "attend: workspace is NULL");
   if (!aligned(workspace, 256)) return fail(MQ_E_ALIGN, "attend: workspace not 256-byte aligned");
-  const size_t need = mq::attend_workspace(batch, q_heads, c->kv_heads, c->head_dim);
+  const size_t need = mq::attend_workspace_need(batch, q_heads, c->kv_heads, c->head_dim);
   if (workspace_bytes < need)
     return fail(MQ_E_WORKSPACE, "attend: workspace %zu bytes, need %zu", workspace_bytes, need);
   mq::AttendArgs a;

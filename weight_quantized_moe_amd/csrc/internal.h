@@ -229,7 +229,8 @@ struct AttendArgs {
   float score_scale;  // scale * k_scale * log2(e): scores are exponents of 2
   float v_scale;
 };
-size_t attend_workspace(int64_t B, int Hq, int Hk, int D);
+size_t attend_workspace(int64_t B, int Hq, int Hk, int D);       // for up to B requests
+size_t attend_workspace_need(int64_t B, int Hq, int Hk, int D);  // of a call with B
 hipError_t launch_attend(const AttendArgs &a, int fp8, hipStream_t s);
 
 // The forward path behind moe_quant_forward and its allocation-free variant:
