@@ -521,9 +521,9 @@ mq_status moe_quant_linear_workspace_size(const mq_linear *l, int64_t num_tokens
  *   x_bf16        [T, K] BF16 bits, 16-byte aligned
  *   residual_bf16 NULL, or [T, N] BF16 bits, 2-byte aligned
  *   out           [T, N] of out_dtype, aligned to its element; a BF16 one may be
- *                 residual_bf16 itself; otherwise it overlaps neither input
+ *                 residual_bf16 itself; otherwise it overlaps nothing that is read
  *   workspace     >= moe_quant_linear_workspace_size bytes, 256-byte aligned; its
- *                 contents on entry do not matter
+ *                 contents on entry do not matter; overlaps nothing else
  * num_tokens == 0 returns MQ_OK without enqueuing anything.
  * Errors: MQ_E_NULL, MQ_E_ABI, MQ_E_SHAPE, MQ_E_DTYPE, MQ_E_ALIGN,
  * MQ_E_WORKSPACE, MQ_E_HIP.
@@ -586,7 +586,8 @@ typedef struct {
  *               is negative or behind the cache, or whose position is not a row of
  *               cos_sin, is padding: nothing of it is written
  *   q_out       [T, q_heads, D] BF16 bits, 16-byte aligned; may be q itself where
- *               q_stride is q_heads * D, and does not overlap q, k and v otherwise
+ *               q_stride is q_heads * D, and overlaps nothing else that is read
+ * The cache's k and v overlap neither each other nor q_out nor what is read.
  * MQ_KV_FP8 keeps RNE-to-E4M3(value / scale), one IEEE FP32 division, saturated to
  * +-448.  The slots of one call are distinct: of a slot given twice it is
  * unspecified which token's values stay, per 8 values.
@@ -621,10 +622,10 @@ mq_status moe_quant_attend_workspace_size(const mq_kv_cache *c, int32_t q_heads,
  *   lengths     int32 [B]; below 1 the request is empty: out 0, lse -inf.  More
  *               than max_pages pages hold counts as what they hold
  *   out_bf16    [B, q_heads, D] BF16 bits, 16-byte aligned; may be q_bf16 itself, and
- *               does not overlap it otherwise
+ *               overlaps nothing else that is read
  *   lse         NULL, or float [B, q_heads], 4-byte aligned
  *   workspace   >= moe_quant_attend_workspace_size bytes, 256-byte aligned; its
- *               contents on entry do not matter
+ *               contents on entry do not matter; lse and it overlap nothing else
  * Tokens on a page outside of [0, num_pages) count as absent.  What the cache
  * holds behind a request's last token, NaN among it, does not reach the result;
  * queries, keys and values of the tokens themselves are finite.  Repeated calls

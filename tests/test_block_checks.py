@@ -314,3 +314,54 @@ def test_attend_workspace_does_not_shrink_with_the_batch(lib):
             assert lib.moe_quant_attend_workspace_size(c, hq, batch, ctypes.byref(b)) == OK
             assert b.value >= last, (heads, hq, d, batch)
             last = b.value
+
+
+# ---------------------------------------------------------------- what must not overlap
+BIG = 1 << 40            # addresses far from each other, that no refused call reads
+
+
+def test_linear_refuses_overlaps_of_what_it_writes(lib):
+    # n 128, k 256, 3 rows: x 0x600 bytes, a BF16 out and the residual 0x300, w 0x8000, scale 8
+    w, sc, x, res, out, ws = (BIG * i for i in range(1, 7))
+    d, b = _linear(w=w, scale=sc), ctypes.c_size_t()
+    assert lib.moe_quant_linear_workspace_size(ctypes.byref(d), 3, ctypes.byref(b)) == OK
+    n = b.value
+    for over in (dict(out=w), dict(out=w + 0x7FFE), dict(out=w - 0x2FE), dict(out=sc + 4), dict(out=ws), dict(out=ws + n - 2),
+                 dict(out=ws - 0x2FE), dict(ws=w + 0x7F00), dict(ws=w - 256), dict(ws=sc), dict(ws=x), dict(ws=x + 0x500),
+                 dict(ws=res + 0x200), dict(ws=res - 256), dict(ws=out)):
+        f = dict(dict(x=x, res=res, out=out, ws=ws), **over)
+        assert lib.moe_quant_linear(ctypes.byref(d), f["x"], f["res"], 3, f["out"], f["ws"], n, None) == SHAPE, over
+
+
+def test_append_refuses_overlaps_of_what_it_writes(lib):
+    # a cache of 10 pages of 16 tokens and 4 heads of 64: 0x14000 bytes each of k and v in BF16
+    kc, vc, cs, qn, kn, q, k, v, pos, slots, out = (BIG * i for i in range(1, 12))
+    for over in (dict(vc=kc), dict(vc=kc + 0x13FF0), dict(vc=kc - 0x13FF0), dict(out=kc), dict(out=kc - 0xBF0),
+                 dict(out=vc + 0x13FF0), dict(out=slots - 0xBF0), dict(out=pos), dict(out=cs + 100 * 128 - 16), dict(out=qn),
+                 dict(out=kn - 16), dict(q=kc), dict(q=vc + 0x13FF0), dict(k=kc), dict(k=vc - 16), dict(v=vc), dict(v=kc + 16),
+                 dict(slots=kc), dict(slots=vc + 0x13FFC), dict(pos=kc - 8), dict(cs=kc + 16), dict(cs=vc - 16), dict(qn=kc),
+                 dict(kn=vc + 16)):
+        f = dict(dict(kc=kc, vc=vc, cs=cs, qn=qn, kn=kn, q=q, k=k, v=v, pos=pos, slots=slots, out=out), **over)
+        c, r = _cache(k=f["kc"], v=f["vc"]), _rotary(c=f["cs"], qn=f["qn"], kn=f["kn"])
+        got = lib.moe_quant_kv_append(ctypes.byref(c), ctypes.byref(r), 8, f["q"], 512, f["k"], 256, f["v"], 256, f["pos"],
+                                      f["slots"], 3, f["out"], None)
+        assert got == SHAPE, over
+    # of an E4M3 cache half as many bytes
+    c, r = _cache(dtype=1, k=kc, v=kc + 0xA000 - 16), _rotary(c=cs)
+    assert lib.moe_quant_kv_append(ctypes.byref(c), ctypes.byref(r), 0, None, 0, k, 256, v, 256, pos, slots, 3, None, None) == SHAPE
+
+
+def test_attend_refuses_overlaps_of_what_it_writes(lib):
+    # 5 requests of 8 heads of 64: q and out 0x1400 bytes, lse 0xA0, 7 pages a request 9 entries apart
+    kc, vc, q, table, lengths, out, lse, ws = (BIG * i for i in range(1, 9))
+    b = ctypes.c_size_t()
+    assert lib.moe_quant_attend_workspace_size(ctypes.byref(_cache()), 8, 5, ctypes.byref(b)) == OK
+    n = b.value
+    for over in (dict(out=kc), dict(out=vc + 0x13FF0), dict(out=ws), dict(out=ws + n - 16), dict(out=lengths), dict(out=lse - 16),
+                 dict(out=table + 160), dict(lse=out + 0x13FC), dict(lse=q), dict(lse=kc + 4), dict(lse=vc - 0x9C),
+                 dict(lse=ws + n - 4), dict(lse=lengths + 16), dict(lse=table + 4 * (4 * 9 + 6)), dict(lse=q, out=q),
+                 dict(ws=q), dict(ws=kc), dict(ws=vc + 0x13F00), dict(ws=table), dict(ws=lengths)):
+        f = dict(dict(kc=kc, vc=vc, q=q, table=table, lengths=lengths, out=out, lse=lse, ws=ws), **over)
+        c = ctypes.byref(_cache(k=f["kc"], v=f["vc"]))
+        got = lib.moe_quant_attend(c, 8, 0.1, 0, f["q"], f["table"], 9, 7, f["lengths"], 5, f["out"], f["lse"], f["ws"], n, None)
+        assert got == SHAPE, over

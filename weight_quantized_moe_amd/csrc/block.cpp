@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "internal.h"
 
@@ -14,6 +15,16 @@ namespace {
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
   return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+// Memory that a call reads or writes (p: NULL where it is not given).
+struct Bytes {
+  const void *p;
+  size_t n;
+};
+bool meets(const Bytes &a, std::initializer_list<Bytes> others) {
+  for (const Bytes &b : others)
+    if (a.p && b.p && overlap(a.p, a.n, b.p, b.n)) return true;
+  return false;
 }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -79,6 +90,10 @@ mq_status check_cache(const mq_kv_cache *c, const char *who) {
   if (!aligned(c->k, 16) || !aligned(c->v, 16))
     return fail(MQ_E_ALIGN, "%s: the cache's k and v must be 16-byte aligned", who);
   return MQ_OK;
+}
+
+size_t cache_bytes(const mq_kv_cache *c) {
+  return (size_t)(c->num_pages * c->page_size) * c->kv_heads * c->head_dim * (c->dtype == MQ_KV_BF16 ? 2 : 1);
 }
 
 mq_status check_rotary(const mq_rotary *r, const mq_kv_cache *c, const char *who) {
@@ -152,6 +167,10 @@ mq_status moe_quant_linear(const mq_linear *l, const uint16_t *x_bf16, const uin
   const LinearWs w = linear_ws(num_tokens, l->k);
   if (workspace_bytes < w.total)
     return fail(MQ_E_WORKSPACE, "linear: workspace %zu bytes, need %zu", workspace_bytes, w.total);
+  const Bytes o = {out, values * (bf16 ? 2 : 4)}, ws = {workspace, w.total}, wt = {l->w, (size_t)l->n * l->k},
+              sc = {l->scale, (size_t)((l->n + 127) / 128) * ((l->k + 127) / 128) * 4};
+  if (meets(o, {ws, wt, sc}) || meets(ws, {{x_bf16, (size_t)num_tokens * l->k * 2}, {residual_bf16, values * 2}, wt, sc}))
+    return fail(MQ_E_SHAPE, "linear: out and workspace must not overlap each other, the weight, the scale or an input");
   mq::LinearArgs a;
   a.x = x_bf16; a.residual = residual_bf16; a.w = l->w; a.scale = l->scale; a.out = out;
   a.codes = (uint8_t *)workspace + w.codes;
@@ -199,6 +218,15 @@ mq_status moe_quant_kv_append(const mq_kv_cache *c, const mq_rotary *r, int32_t 
   if (q && (overlap(q_out, out_bytes, k, span(k_stride, kv)) || overlap(q_out, out_bytes, v, span(v_stride, kv)) ||
             (q_out != q && overlap(q_out, out_bytes, q, span(q_stride, q_heads * D)))))
     return fail(MQ_E_SHAPE, "kv_append: q_out may be q itself but must not overlap q, k and v otherwise");
+  const Bytes kc = {c->k, cache_bytes(c)}, vc = {c->v, cache_bytes(c)}, qo = {q_out, out_bytes},
+              at = {slots, (size_t)num_tokens * 4}, pos = {r->rot_dim ? positions : nullptr, (size_t)num_tokens * 4},
+              cs = {r->cos_sin, (size_t)r->max_positions * r->rot_dim * 4}, qn = {r->q_norm, (size_t)D * 2},
+              kn = {r->k_norm, (size_t)D * 2};
+  if (meets(qo, {kc, vc, at, pos, cs, qn, kn}) || meets(kc, {vc}))
+    return fail(MQ_E_SHAPE, "kv_append: q_out and the cache's k and v must not overlap each other or what is read");
+  for (const Bytes &cache : {kc, vc})
+    if (meets(cache, {{q, span(q_stride, q_heads * D)}, {k, span(k_stride, kv)}, {v, span(v_stride, kv)}, at, pos, cs, qn, kn}))
+      return fail(MQ_E_SHAPE, "kv_append: the cache's k and v must not overlap what the call reads");
   mq::KvAppendArgs a;
   a.q = q; a.k = k; a.v = v;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
@@ -261,6 +289,11 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
   const size_t need = mq::attend_workspace_need(batch, q_heads, c->kv_heads, c->head_dim);
   if (workspace_bytes < need)
     return fail(MQ_E_WORKSPACE, "attend: workspace %zu bytes, need %zu", workspace_bytes, need);
+  const Bytes kc = {c->k, cache_bytes(c)}, vc = {c->v, cache_bytes(c)}, o = {out_bf16, q_bytes}, ws = {workspace, need},
+              l = {lse, (size_t)(batch * q_heads) * 4}, len = {lengths, (size_t)batch * 4},
+              tab = {block_table, (size_t)((batch - 1) * table_stride + max_pages) * 4}, q = {q_bf16, q_bytes};
+  if (meets(o, {kc, vc, ws, l, len, tab}) || meets(l, {kc, vc, ws, len, tab, q}) || meets(ws, {kc, vc, len, tab, q}))
+    return fail(MQ_E_SHAPE, "attend: out, lse and workspace must not overlap each other, the cache or an input");
   mq::AttendArgs a;
   a.q = q_bf16; a.kc = c->k; a.vc = c->v; a.table = block_table; a.lengths = lengths;
   a.table_stride = table_stride; a.out = out_bf16; a.lse = lse; a.ws = workspace;
