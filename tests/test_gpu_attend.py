@@ -367,3 +367,54 @@ def test_one_workspace_for_every_batch():
         torch.cuda.synchronize()
         # cut elsewhere: half a step each
         assert torch.allclose(got.float(), want[:b].float(), rtol=2.0 ** -6, atol=1e-4), b
+
+
+def _way(c, window=0):
+    """(units, whether the call splits them): a plan of pieces for up to 1024 requests whose
+    pages hold more tiles of 32 tokens than the least of a piece."""
+    b, hq, _ = c.q.shape
+    hk, page = c.k.shape[1:3]
+    units = b * hk * -(-(hq // hk) // 16)
+    tokens = c.table.shape[1] * page
+    tokens = min(window + 31, tokens) if window else tokens
+    return units, b <= 1024 and -(-tokens // 32) > min(128, max(4, units // 8))
+
+
+@pytest.mark.parametrize("hq", [1, 3, 5, 7, 20])
+@pytest.mark.parametrize("d", [64, 96, 128, 208, 256])
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_many_units_in_pieces(hq, d, dtype):
+    """Above 64 units a wave joins a head: any number of heads, one and two passes over D,
+    pieces beyond the ones asked for ahead."""
+    rng = np.random.default_rng(hq + d)
+    lengths = [int(n) for n in rng.integers(0, 150, 70)]
+    lengths[11], lengths[40] = 3000, 5000
+    c = Case(lengths, hq, 1, d, page=32, dtype=dtype, seed=hq)
+    units, split = _way(c)
+    assert units > 64 and split
+    c.check()
+
+
+@pytest.mark.parametrize("batch", [65, 257, 300, 700, 1023, 1024])
+def test_plans_of_many_requests(batch):
+    rng = np.random.default_rng(batch)
+    lengths = [int(n) for n in rng.integers(0, 40, batch)]
+    lengths[batch // 3], lengths[-1] = 4500, 6000
+    for window in (0, 5000):
+        c = Case(lengths, 6, 2, 64, page=64, seed=batch)
+        units, split = _way(c, window)
+        assert units == 2 * batch and split
+        c.check(window=window)
+
+
+@pytest.mark.parametrize("batch,n,hq,hk", [(5, 400, 8, 2), (5, 9000, 8, 2), (70, 700, 4, 1), (70, 3000, 20, 1), (1100, 100, 4, 2)])
+def test_equal_requests_have_equal_bits(batch, n, hq, hk):
+    c = Case([n], hq, hk, 64, seed=20)
+    table, lengths, q = c.table.repeat(batch, 1), c.lengths.repeat(batch), c.q.repeat(batch, 1, 1)
+    lse = torch.empty(batch, hq, device="cuda")
+    out = c.cache.attend(q, table, lengths, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    ref = f64(c.check()[0][0])
+    # the request alone may be cut elsewhere: each half a step off, and both within the sums' errors
+    assert np.all(np.abs(f64(out[0]) - ref) <= 2.0 ** -6 * np.abs(ref) + 1e-4)
