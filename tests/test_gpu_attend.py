@@ -418,3 +418,23 @@ def test_equal_requests_have_equal_bits(batch, n, hq, hk):
     ref = f64(c.check()[0][0])
     # the request alone may be cut elsewhere: each half a step off, and both within the sums' errors
     assert np.all(np.abs(f64(out[0]) - ref) <= 2.0 ** -6 * np.abs(ref) + 1e-4)
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 + 5, 2 ** 64 + 1])
+def test_windows_beyond_32_bits(window):
+    """As large as any request, and no window of the low 32 bits; the negative ones are refused."""
+    c = Case([300, 70, 0], seed=22)
+    want = c.cache.attend(c.q, c.table, c.lengths)
+    got = c.cache.attend(c.q, c.table, c.lengths, window=window)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    with pytest.raises(MoeQuantError):
+        c.cache.attend(c.q, c.table, c.lengths, window=-window)
+
+
+def test_a_table_beyond_32_bits_of_pages():
+    c = Case([300], seed=23)
+    wide = torch.empty(1, 2 ** 32 + c.table.shape[1], dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    with pytest.raises(MoeQuantError):
+        c.cache.attend(c.q, wide, c.lengths)

@@ -622,7 +622,8 @@ class Linear:
         self.n, self.k, self.out_dtype, self.device = n, k, out_dtype, w.device
         self._keep = (w, w_scale)
         self._q, self._call, self._index = _get_quick(), self._lib.moe_quant_linear, w.get_device()
-        self.desc = LinearDesc(ABI_VERSION, n, k, _mq_dtype(out_dtype), _ptr(w), _ptr(w_scale))
+        self.desc = LinearDesc(ABI_VERSION, min(n, 2 ** 31 - 1), min(k, 2 ** 31 - 1), _mq_dtype(out_dtype), _ptr(w),
+                               _ptr(w_scale))
         self._ref = ctypes.byref(self.desc)
         self._last_need = (-1, 0)      # (tokens, bytes) of the last call
         self.workspace_size(0)         # the library's own checks of the fields
@@ -857,6 +858,8 @@ class KVCache:
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
             _on_gpu(self.device, q=q, out=out, block_table=block_table, lengths=lengths, lse=lse, workspace=workspace)
+        if not (0 <= window < 2 ** 31 and pages < 2 ** 31):     # ctypes would pass their low 32 bits on
+            window, pages = -1 if window < 0 else min(window, 2 ** 31 - 1), min(pages, 2 ** 31 - 1)
         st = self._attend(self._ref, hq, d ** -0.5 if scale is None else scale, window, q.data_ptr(),
                           block_table.data_ptr(), apart, pages, lengths.data_ptr(), b, out.data_ptr(),
                           None if lse is None else lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
