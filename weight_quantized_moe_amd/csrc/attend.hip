@@ -18,12 +18,13 @@
 // p = hi + lo (2^-17 of p is lost): with one BF16 value their rounding (2^-9)
 // would be as large an error as the output's own rounding.
 //
-// Bound by the cache's bytes, which are read once: 64 requests of 1 to 8192 tokens
-// (32 query heads on 4 key heads of 128, BF16, 538 MB) take 108 us, 5.0 TB/s, where a
-// large copy moves 5.4; four of 100000 to 131072 in E4M3 (473 MB) 90 us, 5.3 TB/s.  The
+// Bound by the cache's bytes, which are read once (of more than 16 heads per key head once
+// for each 16): a call of 64 requests of 1 to 8192 tokens (32 query heads on 4 key heads
+// of 128, BF16, 540 MB) takes 107 to 116 us by the lengths drawn, 4.8 to 5.0 TB/s, where a
+// large copy moves 5.4; four of 100000 to 131072 in E4M3 (473 MB) 92 us, 5.1 TB/s.  The
 // matrix units are busy 4 to 10% of that time and the vector units 20 to 40%, so the
 // 16 columns that fewer shared heads leave empty cost nothing that would be
-// missed.  A wave has two tiles' loads in flight (16 KB each at D = 128 in BF16) and
+// missed.  D above 128, without a tile ahead: 192 170 us of 810 MB, 256 215 us of 1080.  A wave has two tiles' loads in flight (16 KB each at D = 128 in BF16) and
 // a CU 8 waves, so memory is kept busy without LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -55,7 +56,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 constexpr int kTile = 32;    // tokens of one step of a wave
 constexpr int kWaves = 4;
-// Requests that the pieces' plan goes through; a workgroup takes whole units above it.
+// Requests that the pieces' plan goes through; a workgroup takes whole units above it:
+// every wave walks the lengths twice, which with 4097 requests of up to 600 tokens and one
+// of 20000 costs more than the long one alone on its workgroups (2268 us, whole 763).  At
+// 1025 of up to 8192 whole is no slower (1487 us, in pieces 1508), but one of 100000 among
+// 1024 of up to 2000 is (1681, in pieces 595).
 constexpr int kPlanBatch = 1024;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -509,7 +514,10 @@ int groups_of(int64_t units) {
 }
 // Tiles of a piece at least: with few units one per wave (4 units of 32 tiles:
 // 11.4 us, 12.8 with two per wave), with many as much as keeps a unit whole that the
-// other units' workgroups hide (396 units of 32 tiles: 24 us whole, 31 in two).
+// other units' workgroups hide (396 units of 32 tiles: 24 us whole, 31 in two).  Whole
+// calls by this rule and with 4 tiles at least, key heads 4: 32 requests of 500 tokens
+// 11.8 and 15.3 us, 64 of 500 17.3 and 27.2, 32 of 1000 22.7 and 27.3, 99 of 1000 42.1 and
+// 54.6; 16 of 500 13.1 and 12.1, 48 of 2000 53.7 and 49.4.
 int share_min_of(int64_t units) { return units / 8 < 4 ? 4 : units / 8 > 128 ? 128 : (int)(units / 8); }
 
 }  // namespace

@@ -10,13 +10,15 @@
 // (exact) and go through four 16x16x32 FP16 instructions, whose sums are FP32
 // ones (2^-23.7 of the largest product in the mean), at half the rate.
 //
-// For many tokens bound by instructions: at 8192^3 the 256 x 256 tiles run at 2260
-// TFLOP/s (the quantization aside), with the matrix units busy half of the cycles
-// and the vector units 41%, mostly the four scaling sums per matrix instruction (a copy
-// without those ran 13% faster, one without the copies into LDS 20%); the library's
-// product of E4M3 tensors with one scale each reaches 2716.  16384 x 5120 x 2048: 178 us
-// (1930 TFLOP/s), about a tenth of it the tiles' starts and ends, after 21 us for the
-// quantization (100 MB).  For few tokens bound by launches and latency.
+// For many tokens bound by instructions: at 8192^3 the 256 x 256 tiles take 510 us in the
+// median (2155 TFLOP/s, the quantization aside; 482 at the least), with the matrix units
+// busy 52% of the cycles and the vector units 40%, mostly the four scaling sums per matrix
+// instruction (a copy without those ran 13% faster, one without the copies into LDS
+// 20%); the library's product of E4M3 tensors with one scale each reaches 2716 TFLOP/s.
+// 16384 x 5120 x 2048: 187 to 196 us (1750 to 1840 TFLOP/s; 178 at the least), about a
+// tenth of it the tiles' starts and ends, after 24 us for the quantization (100 MB).
+// Outputs of N % 8 != 0 are stored value by value (8192 x 5121: 192 us a call, x 5120
+// 118).  For few tokens bound by launches and latency.
 //
 // Three ways through it:
 //   few tokens     one launch: every workgroup quantizes the rows itself
