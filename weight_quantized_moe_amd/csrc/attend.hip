@@ -23,9 +23,10 @@
 // of 128, BF16, 540 MB) takes 107 to 116 us by the lengths drawn, 4.8 to 5.0 TB/s, where a
 // large copy moves 5.4; four of 100000 to 131072 in E4M3 (473 MB) 92 us, 5.1 TB/s.  The
 // matrix units are busy 4 to 10% of that time and the vector units 20 to 40%, so the
-// 16 columns that fewer shared heads leave empty cost nothing that would be
-// missed.  D above 128, without a tile ahead: 192 170 us of 810 MB, 256 215 us of 1080.  A wave has two tiles' loads in flight (16 KB each at D = 128 in BF16) and
-// a CU 8 waves, so memory is kept busy without LDS.
+// 16 columns that fewer shared heads leave empty cost nothing that would be missed.  A
+// wave has two tiles' loads in flight (16 KB each at D = 128 in BF16) and a CU 8 waves, so
+// memory is kept busy without LDS.  D above 128 has no tile ahead: those 64 requests take
+// 170 us at 192 (810 MB) and 215 at 256 (1080 MB).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

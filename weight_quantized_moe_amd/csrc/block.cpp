@@ -291,7 +291,7 @@ mq_status moe_quant_attend(const mq_kv_cache *c, int32_t q_heads, float scale, i
     return fail(MQ_E_WORKSPACE, "attend: workspace %zu bytes, need %zu", workspace_bytes, need);
   const Bytes kc = {c->k, cache_bytes(c)}, vc = {c->v, cache_bytes(c)}, o = {out_bf16, q_bytes}, ws = {workspace, need},
               l = {lse, (size_t)(batch * q_heads) * 4}, len = {lengths, (size_t)batch * 4},
-              tab = {block_table, (size_t)((batch - 1) * table_stride + max_pages) * 4}, q = {q_bf16, q_bytes};
+              tab = {block_table, ((size_t)(batch - 1) * (size_t)table_stride + max_pages) * 4}, q = {q_bf16, q_bytes};
   if (meets(o, {kc, vc, ws, l, len, tab}) || meets(l, {kc, vc, ws, len, tab, q}) || meets(ws, {kc, vc, len, tab, q}))
     return fail(MQ_E_SHAPE, "attend: out, lse and workspace must not overlap each other, the cache or an input");
   mq::AttendArgs a;
